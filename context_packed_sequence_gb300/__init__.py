@@ -13,6 +13,10 @@ from .api import (  # noqa: F401
     pack_rank, scatter_rank, ulysses_swap,
     roll_labels, roll_labels_zigzag, pack_docs, zigzag_contiguous_thd_swap,
 )
+from .losses import (  # noqa: F401
+    TOKEN_MEAN, DOC_MEAN, TOKEN_SUM, PolicyLoss, PreferenceLoss, DistillLoss,
+    loss_weights, token_logprobs, token_logprobs_backward, policy_loss, preference_loss, distill_topk_loss,
+)
 from .exchange import CpExchange  # noqa: F401
 from . import _lib  # noqa: F401
 

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_int32, c_int64, c_size_t, c_void_p, c_char_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p, c_char_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libthd.so")
 # THD_CHECKED=1 in the environment: the debug build, whose kernels range-check
@@ -57,6 +57,15 @@ SEQ_TO_HEAD = 0
 HEAD_TO_SEQ = 1
 MAX_CP = 64
 
+# thd_dtype_t, thd_reduction_t
+DTYPE_F32 = 0
+DTYPE_BF16 = 1
+DTYPE_F16 = 2
+TOKEN_MEAN = 0
+DOC_MEAN = 1
+TOKEN_SUM = 2
+MAX_TEACHER_ENTRIES = 1024
+
 
 class ThdRoute(ctypes.Structure):
     """Mirror of thd_route_t."""
@@ -74,6 +83,36 @@ class ThdRoute(ctypes.Structure):
         ("recv_identity", c_void_p),
         ("src_of_dst", c_void_p),
     ]
+
+
+class ThdLogits(ctypes.Structure):
+    """Mirror of thd_logits_t."""
+    _fields_ = [("data", c_void_p), ("rows", c_int64), ("row_stride", c_int64), ("vocab", c_int32),
+                ("dtype", c_int32), ("temperature", c_float), ("reserved", c_int32)]
+
+
+class ThdGradient(ctypes.Structure):
+    """Mirror of thd_gradient_t."""
+    _fields_ = [("dlogits", c_void_p), ("row_stride", c_int64), ("scale", c_float), ("reserved", c_int32)]
+
+
+class ThdPolicy(ctypes.Structure):
+    """Mirror of thd_policy_t."""
+    _fields_ = [("old_logprobs", c_void_p), ("ref_logprobs", c_void_p), ("advantages", c_void_p),
+                ("doc_ids", c_void_p), ("num_docs", c_int32), ("clip_low", c_float), ("clip_high", c_float),
+                ("kl_coef", c_float)]
+
+
+class ThdPreference(ctypes.Structure):
+    """Mirror of thd_preference_t."""
+    _fields_ = [("ref_logprobs", c_void_p), ("beta", c_float), ("label_smoothing", c_float), ("margin", c_float),
+                ("length_normalized", c_int32)]
+
+
+class ThdTeacher(ctypes.Structure):
+    """Mirror of thd_teacher_t."""
+    _fields_ = [("ids", c_void_p), ("scores", c_void_p), ("count", c_int32), ("dtype", c_int32),
+                ("normalize", c_int32), ("reserved", c_int32)]
 
 
 # name -> (restype, argtypes), one entry per function declared in include/thd.h
@@ -107,6 +146,21 @@ SIGNATURES = {
                                 c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "thd_pack_docs_noalloc": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_int32, c_int32, c_int32, c_int32,
                                         c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                                        c_void_p]),
+    "thd_loss_weights_workspace_bytes": (c_size_t, [c_int32]),
+    "thd_loss_weights": (c_int32, [c_void_p, c_void_p, c_int32, c_int64, c_int32, c_int32, c_void_p, c_void_p,
+                                   c_void_p, c_size_t, c_void_p, c_void_p]),
+    "thd_token_logprobs": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "thd_token_logprobs_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_void_p]),
+    "thd_policy_loss_workspace_bytes": (c_size_t, [c_int64]),
+    "thd_policy_loss": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_size_t, c_void_p, c_void_p]),
+    "thd_preference_loss_workspace_bytes": (c_size_t, [c_int32]),
+    "thd_preference_loss": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p,
+                                      c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_size_t, c_void_p, c_void_p]),
+    "thd_distill_topk_loss": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_void_p]),
     "thd_status_clear": (c_int32, [c_void_p, c_void_p]),
     "thd_status_read": (c_int32, [c_void_p, POINTER(c_int32), c_void_p]),

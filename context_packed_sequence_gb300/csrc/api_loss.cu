@@ -1,0 +1,228 @@
+// extern "C" entry points of the losses: host-side argument checks, then the
+// launches on the caller's stream.  See include/thd.h for the contracts.
+#include <climits>
+#include <cmath>
+
+#include "loss_internal.cuh"
+
+namespace thd {
+namespace {
+
+constexpr int64_t kMaxRows = INT32_MAX;
+
+int64_t dtype_bytes(int32_t dtype) {
+  switch (dtype) {
+    case THD_DTYPE_F32: return 4;
+    case THD_DTYPE_BF16:
+    case THD_DTYPE_F16: return 2;
+    default: return 0;
+  }
+}
+
+bool element_aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+bool logits_ok(const thd_logits_t* z) {
+  if (!z || z->rows < 0 || z->rows > kMaxRows || z->vocab < 1 || z->row_stride < z->vocab) return false;
+  const int64_t e = dtype_bytes(z->dtype);
+  if (e == 0 || z->row_stride > INT64_MAX / 8 / (z->rows + 1)) return false;
+  if (!(z->temperature >= 1e-4f && z->temperature <= 1e4f)) return false;
+  return z->rows == 0 || (z->data && element_aligned(z->data, e));
+}
+
+// bytes from a matrix' first element to one past its last
+int64_t span(int64_t rows, int64_t stride, int32_t cols, int64_t e) {
+  return rows == 0 ? 0 : ((rows - 1) * stride + cols) * e;
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+bool gradient_ok(const thd_logits_t* z, const thd_gradient_t* g) {
+  if (!std::isfinite(g->scale) || g->row_stride < z->vocab) return false;
+  if (g->row_stride > INT64_MAX / 8 / (z->rows + 1)) return false;
+  if (z->rows == 0) return true;
+  const int64_t e = dtype_bytes(z->dtype);
+  if (!g->dlogits || !element_aligned(g->dlogits, e)) return false;
+  if (g->dlogits == z->data && (g->row_stride == z->row_stride || z->rows == 1)) return true;
+  return !overlap(z->data, span(z->rows, z->row_stride, z->vocab, e), g->dlogits,
+                  span(z->rows, g->row_stride, z->vocab, e));
+}
+
+RowArgs row_args(const thd_logits_t* z, const thd_gradient_t* g, int32_t* status) {
+  RowArgs a = {};
+  a.logits = z->data;
+  a.stride = z->row_stride;
+  a.rows = static_cast<int32_t>(z->rows);
+  a.vocab = z->vocab;
+  a.scale = make_logit_scale(z->temperature);
+  a.status = status;
+  if (g) {
+    a.dlogits = g->dlogits;
+    a.dstride = g->row_stride;
+    a.grad_scale = g->scale;
+  }
+  return a;
+}
+
+// documents of T rows in the layout of cp ranks
+bool documents_ok(const int32_t* cu, int32_t num_docs, int64_t T, int32_t cp) {
+  if (!cu || num_docs < 0 || num_docs > kMaxRows - 1 || T < 0 || T > kMaxRows) return false;
+  return cp >= 1 && cp <= THD_MAX_CP && (cp == 1 || T % (2 * cp) == 0);
+}
+
+bool workspace_ok(const void* p, size_t have, size_t need) {
+  return need == 0 || (p && have >= need && reinterpret_cast<uintptr_t>(p) % 4 == 0);
+}
+
+}  // namespace
+}  // namespace thd
+
+using namespace thd;
+
+extern "C" {
+
+size_t thd_loss_weights_workspace_bytes(int32_t num_docs) {
+  return num_docs < 0 ? 0 : static_cast<size_t>(num_docs) * sizeof(int32_t);
+}
+
+thd_status_t thd_loss_weights(const uint8_t* loss_mask, const int32_t* cu_seqlens_padded, int32_t num_docs, int64_t T,
+                              int32_t cp_size, int32_t reduction, float* weights, int32_t* doc_ids, void* workspace,
+                              size_t workspace_bytes, int32_t* d_status, cudaStream_t stream) {
+  if (!documents_ok(cu_seqlens_padded, num_docs, T, cp_size)) return THD_ERR_INVALID_ARG;
+  if (reduction != THD_TOKEN_MEAN && reduction != THD_DOC_MEAN && reduction != THD_TOKEN_SUM)
+    return THD_ERR_INVALID_ARG;
+  if (T > 0 && (!loss_mask || !weights)) return THD_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, thd_loss_weights_workspace_bytes(num_docs)))
+    return THD_ERR_INVALID_ARG;
+  return launch_loss_weights(loss_mask, cu_seqlens_padded, num_docs, static_cast<int32_t>(T), cp_size, reduction,
+                             weights, doc_ids, static_cast<int32_t*>(workspace), d_status, stream);
+}
+
+thd_status_t thd_token_logprobs(const thd_logits_t* logits, const int32_t* labels, const uint8_t* loss_mask,
+                                float* logprobs, float* lse, int32_t* d_status, cudaStream_t stream) {
+  if (!logits_ok(logits)) return THD_ERR_INVALID_ARG;
+  if (logits->rows > 0 && (!labels || !logprobs || !lse)) return THD_ERR_INVALID_ARG;
+  RowArgs a = row_args(logits, nullptr, d_status);
+  a.labels = labels;
+  a.mask = loss_mask;
+  a.logprobs = logprobs;
+  a.lse = lse;
+  return launch_row_loss(ROW_SCORE, logits->dtype, a, stream);
+}
+
+thd_status_t thd_token_logprobs_backward(const thd_logits_t* logits, const int32_t* labels, const float* lse,
+                                         const float* dlogprobs, const thd_gradient_t* gradient, int32_t* d_status,
+                                         cudaStream_t stream) {
+  if (!logits_ok(logits) || !gradient || !gradient_ok(logits, gradient)) return THD_ERR_INVALID_ARG;
+  if (logits->rows > 0 && (!labels || !lse || !dlogprobs)) return THD_ERR_INVALID_ARG;
+  RowArgs a = row_args(logits, gradient, d_status);
+  a.labels = labels;
+  return launch_logprobs_backward(logits->dtype, a, lse, dlogprobs, stream);
+}
+
+size_t thd_policy_loss_workspace_bytes(int64_t rows) {
+  return rows < 0 || rows > kMaxRows ? 0 : 3 * static_cast<size_t>(rows) * sizeof(float);
+}
+
+thd_status_t thd_policy_loss(const thd_logits_t* logits, const int32_t* labels, const float* weights,
+                             const thd_policy_t* policy, const thd_gradient_t* gradient, float* logprobs, float* sums,
+                             void* workspace, size_t workspace_bytes, int32_t* d_status, cudaStream_t stream) {
+  if (!logits_ok(logits) || !policy || !sums || (gradient && !gradient_ok(logits, gradient)))
+    return THD_ERR_INVALID_ARG;
+  if (!(policy->clip_low >= 0.0f && policy->clip_low <= 1.0f) || !(policy->clip_high >= 0.0f) ||
+      !std::isfinite(policy->clip_high) || !std::isfinite(policy->kl_coef))
+    return THD_ERR_INVALID_ARG;
+  if (policy->doc_ids && policy->num_docs < 0) return THD_ERR_INVALID_ARG;
+  if (logits->rows > 0 && (!labels || !weights || !logprobs || !policy->old_logprobs ||
+                           (!policy->advantages && !(policy->doc_ids && policy->num_docs == 0))))
+    return THD_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, thd_policy_loss_workspace_bytes(logits->rows)))
+    return THD_ERR_INVALID_ARG;
+  RowArgs a = row_args(logits, gradient, d_status);
+  a.labels = labels;
+  a.weights = weights;
+  a.logprobs = logprobs;
+  a.terms = static_cast<float*>(workspace);
+  a.old_logprobs = policy->old_logprobs;
+  a.ref_logprobs = policy->ref_logprobs;
+  a.advantages = policy->advantages;
+  a.doc_ids = policy->doc_ids;
+  a.num_docs = policy->num_docs;
+  a.ratio_min = 1.0f - policy->clip_low;
+  a.ratio_max = 1.0f + policy->clip_high;
+  a.kl_coef = policy->kl_coef;
+  const thd_status_t r = launch_row_loss(ROW_POLICY, logits->dtype, a, stream);
+  if (r != THD_OK) return r;
+  return launch_final_sums(a.terms, nullptr, 3, logits->rows, sums, d_status, stream);
+}
+
+size_t thd_preference_loss_workspace_bytes(int32_t num_docs) {
+  return num_docs < 0 ? 0 : static_cast<size_t>(num_docs) * (sizeof(float) + sizeof(int32_t));
+}
+
+thd_status_t thd_preference_loss(const float* logprobs, const uint8_t* loss_mask, const int32_t* cu_seqlens_padded,
+                                 int32_t num_docs, int64_t T, int32_t cp_size, const int32_t* chosen,
+                                 const int32_t* rejected, int32_t num_pairs, const thd_preference_t* params,
+                                 float* loss, float* margins, float* doc_logprobs, float* dlogprobs, void* workspace,
+                                 size_t workspace_bytes, int32_t* d_status, cudaStream_t stream) {
+  if (!documents_ok(cu_seqlens_padded, num_docs, T, cp_size) || !params || !loss || num_pairs < 0)
+    return THD_ERR_INVALID_ARG;
+  if (!std::isfinite(params->beta) || !std::isfinite(params->margin) ||
+      !(params->label_smoothing >= 0.0f && params->label_smoothing <= 1.0f))
+    return THD_ERR_INVALID_ARG;
+  if (T > 0 && (!logprobs || !loss_mask || !dlogprobs)) return THD_ERR_INVALID_ARG;
+  if (num_docs > 0 && !doc_logprobs) return THD_ERR_INVALID_ARG;
+  if (num_pairs > 0 && (!chosen || !rejected || !margins)) return THD_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, thd_preference_loss_workspace_bytes(num_docs)))
+    return THD_ERR_INVALID_ARG;
+  PreferenceArgs a = {};
+  a.logprobs = logprobs;
+  a.ref_logprobs = params->ref_logprobs;
+  a.mask = loss_mask;
+  a.cu = cu_seqlens_padded;
+  a.num_docs = num_docs;
+  a.rows = static_cast<int32_t>(T);
+  a.cp = cp_size;
+  a.chosen = chosen;
+  a.rejected = rejected;
+  a.num_pairs = num_pairs;
+  a.beta = params->beta;
+  a.smoothing = params->label_smoothing;
+  a.margin = params->margin;
+  a.length_normalized = params->length_normalized;
+  a.loss = loss;
+  a.margins = margins;
+  a.doc_logprobs = doc_logprobs;
+  a.dlogprobs = dlogprobs;
+  a.gain = static_cast<float*>(workspace);
+  a.count = reinterpret_cast<int32_t*>(a.gain + num_docs);
+  a.status = d_status;
+  return launch_preference(a, stream);
+}
+
+thd_status_t thd_distill_topk_loss(const thd_logits_t* logits, const thd_teacher_t* teacher, const float* weights,
+                                   const thd_gradient_t* gradient, float* token_losses, float* loss,
+                                   int32_t* d_status, cudaStream_t stream) {
+  if (!logits_ok(logits) || !teacher || !loss || (gradient && !gradient_ok(logits, gradient)))
+    return THD_ERR_INVALID_ARG;
+  const int64_t e = dtype_bytes(teacher->dtype);
+  if (teacher->count < 1 || teacher->count > THD_MAX_TEACHER_ENTRIES || e == 0) return THD_ERR_INVALID_ARG;
+  if (logits->rows > 0 && (!teacher->ids || !teacher->scores || !element_aligned(teacher->scores, e) || !weights ||
+                           !token_losses))
+    return THD_ERR_INVALID_ARG;
+  RowArgs a = row_args(logits, gradient, d_status);
+  a.weights = weights;
+  a.token_losses = token_losses;
+  a.teacher_ids = teacher->ids;
+  a.teacher_scores = teacher->scores;
+  a.teacher_dtype = teacher->dtype;
+  a.teacher_count = teacher->count;
+  a.normalize = teacher->normalize;
+  const thd_status_t r = launch_row_loss(ROW_DISTILL, logits->dtype, a, stream);
+  if (r != THD_OK) return r;
+  return launch_final_sums(token_losses, weights, 1, logits->rows, loss, d_status, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,298 @@
+// Losses over documents: row weights from the loss mask, the preference loss
+// over pairs of documents, and the final sums of the row losses.
+//
+// In the zigzag layout of cp ranks document i takes the local slots
+// [cu[i]/cp, cu[i+1]/cp) of every rank, so its rows are cp runs of equal
+// length, and row p = r*S + j belongs to the document that holds slot j.  The
+// contiguous layout is the case cp = 1.
+#include <algorithm>
+
+#include "loss_internal.cuh"
+
+namespace thd {
+namespace {
+
+constexpr int kDocThreads = 256;
+constexpr int kSumThreads = 1024;
+
+// One document's slots [lo, hi) of every rank.  Boundaries that break a rule
+// (reported by the block that checks them all) are clamped into the rows, so
+// nothing outside is touched.
+struct DocSlots {
+  int32_t lo, hi;
+};
+
+__device__ __forceinline__ DocSlots doc_slots(const int32_t* cu, int32_t i, int32_t T, CpMath m) {
+  const int32_t a = min(max(cu[i], 0), T), b = min(max(cu[i + 1], a), T);
+  return {m.div(a), m.div(b)};
+}
+
+// Document of row p (clamped like doc_slots).
+__device__ __forceinline__ int32_t row_document(const int32_t* cu, int32_t n, int32_t slot, CpMath m) {
+  return min(doc_of(cu, n, slot * m.cp), n - 1);
+}
+
+// Sum over the block, the same bits whatever the other blocks do.
+template <typename V>
+__device__ __forceinline__ V block_total(V v, V* tmp) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+  if (lane == 0) tmp[wid] = v;
+  __syncthreads();
+  v = lane < nw ? tmp[lane] : V(0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+  __syncthreads();
+  return v;
+}
+
+// A pair sum over the block: partial sums of many terms lose nothing to rounding.
+__device__ __forceinline__ float block_total_pair(Pair p, Pair* tmp) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    p = add(p, {__shfl_xor_sync(kFullMask, p.hi, o), __shfl_xor_sync(kFullMask, p.lo, o)});
+  if (lane == 0) tmp[wid] = p;
+  __syncthreads();
+  p = lane < nw ? tmp[lane] : Pair{0.0f, 0.0f};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    p = add(p, {__shfl_xor_sync(kFullMask, p.hi, o), __shfl_xor_sync(kFullMask, p.lo, o)});
+  __syncthreads();
+  return p.hi + p.lo;
+}
+
+// ---------------------------------------------------------------------------
+// row weights
+// ---------------------------------------------------------------------------
+
+// Rows with loss of each document: one block per document.  Block 0 also
+// checks the boundaries.
+__global__ void __launch_bounds__(kDocThreads)
+    count_rows_kernel(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t S, CpMath m, int32_t mult,
+                      int32_t* counts, int32_t* st) {
+  pdl_wait_then_release();
+  __shared__ int32_t tmp[32];
+  if (block_status_set(st)) return;
+  if (blockIdx.x == 0) {
+    const int32_t code = block_check_cu(cu, n, T, mult, true);
+    if (code != THD_OK) {
+      if (threadIdx.x == 0) status_set(st, code);
+      return;
+    }
+  }
+  const int32_t i = blockIdx.x;
+  if (i >= n) return;  // the one block of a batch without documents
+  const DocSlots d = doc_slots(cu, i, T, m);
+  int32_t c = 0;
+  for (int32_t r = 0; r < m.cp; ++r)
+    for (int64_t j = d.lo + threadIdx.x; j < d.hi; j += kDocThreads) c += mask[static_cast<int64_t>(r) * S + j] != 0;
+  c = block_total(c, tmp);
+  if (threadIdx.x == 0) counts[i] = c;
+}
+
+__global__ void __launch_bounds__(kDocThreads)
+    loss_weights_kernel(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t S, CpMath m,
+                        int32_t reduction, const int32_t* counts, float* weights, int32_t* doc_ids, const int32_t* st) {
+  pdl_wait_then_release();
+  __shared__ int64_t tmp[32];
+  if (block_status_set(st) || n == 0) return;
+  int64_t part = 0;
+  for (int64_t i = threadIdx.x; i < n; i += kDocThreads) part += reduction == THD_DOC_MEAN ? counts[i] > 0 : counts[i];
+  const float total = static_cast<float>(block_total(part, tmp));
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kDocThreads;
+  for (int64_t p = static_cast<int64_t>(blockIdx.x) * kDocThreads + threadIdx.x; p < T; p += step) {
+    const int32_t slot = static_cast<int32_t>(p % S);
+    const int32_t i = row_document(cu, n, slot, m);
+    float w = 0.0f;
+    if (mask[p]) {
+      if (reduction == THD_TOKEN_SUM) w = 1.0f;
+      else if (reduction == THD_TOKEN_MEAN) w = 1.0f / total;
+      else w = 1.0f / (static_cast<float>(counts[i]) * total);
+    }
+    weights[p] = w;
+    if (doc_ids) doc_ids[p] = i;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// preference loss
+// ---------------------------------------------------------------------------
+
+// Sums of the label log-probabilities of each document, and of their gain
+// over the reference: one block per document.
+__global__ void __launch_bounds__(kDocThreads)
+    doc_sums_kernel(const PreferenceArgs a, int32_t S, CpMath m, int32_t mult) {
+  pdl_wait_then_release();
+  __shared__ Pair pairs[32];
+  __shared__ int32_t tmp[32];
+  if (block_status_set(a.status)) return;
+  if (blockIdx.x == 0) {
+    const int32_t code = block_check_cu(a.cu, a.num_docs, a.rows, mult, true);
+    if (code != THD_OK) {
+      if (threadIdx.x == 0) status_set(a.status, code);
+      return;
+    }
+  }
+  const int32_t i = blockIdx.x;
+  if (i >= a.num_docs) return;
+  const DocSlots d = doc_slots(a.cu, i, a.rows, m);
+  Pair sum = {0.0f, 0.0f}, gain = {0.0f, 0.0f};
+  int32_t c = 0;
+  for (int32_t r = 0; r < m.cp; ++r) {
+    for (int64_t j = d.lo + threadIdx.x; j < d.hi; j += kDocThreads) {
+      const int64_t p = static_cast<int64_t>(r) * S + j;
+      if (!a.mask[p]) continue;  // what a masked row holds is never read
+      const float lp = a.logprobs[p];
+      ++c;
+      sum = add(sum, {lp, 0.0f});
+      // the difference of two close numbers, exactly
+      gain = add(gain, a.ref_logprobs ? two_sum(lp, -a.ref_logprobs[p]) : Pair{lp, 0.0f});
+    }
+  }
+  const float s = block_total_pair(sum, pairs), g = block_total_pair(gain, pairs);
+  c = block_total(c, tmp);
+  if (threadIdx.x == 0) {
+    const float per = a.length_normalized && c > 0 ? static_cast<float>(c) : 1.0f;
+    a.doc_logprobs[i] = s / per;
+    a.gain[i] = g / per;
+    a.count[i] = c;
+  }
+}
+
+struct PairTerm {
+  float h, loss, slope;  // slope: d loss / d h of one pair
+};
+
+__device__ __forceinline__ PairTerm pair_term(const PreferenceArgs& a, int32_t c, int32_t r) {
+  PairTerm t;
+  t.h = a.beta * (a.gain[c] - a.gain[r]);
+  const float x = t.h - a.margin;
+  // -ln sigmoid(x) = max(-x, 0) + ln(1 + exp(-|x|)), and sigmoid from the same exponential
+  const float e = expf(-fabsf(x)), l = log1pf(e);
+  const float neg = fmaxf(-x, 0.0f) + l, pos = fmaxf(x, 0.0f) + l;
+  const float small = e / (1.0f + e), big = 1.0f / (1.0f + e);
+  const float sig = x >= 0.0f ? big : small, sig_neg = x >= 0.0f ? small : big;
+  t.loss = a.smoothing == 0.0f ? neg : (1.0f - a.smoothing) * neg + a.smoothing * pos;
+  t.slope = a.smoothing * sig - (1.0f - a.smoothing) * sig_neg;
+  if (x != x) t.loss = t.slope = x;
+  return t;
+}
+
+__device__ __forceinline__ bool pair_ok(const PreferenceArgs& a, int32_t c, int32_t r) {
+  return c >= 0 && c < a.num_docs && r >= 0 && r < a.num_docs;
+}
+
+// Blocks 0 .. num_docs-1: one document's gradient from every pair it is in,
+// then its rows' gradients.  The last block: every pair's margin and the loss.
+__global__ void __launch_bounds__(kDocThreads) preference_kernel(const PreferenceArgs a, int32_t S, CpMath m) {
+  pdl_wait_then_release();
+  __shared__ Pair pairs[32];
+  if (block_status_set(a.status)) return;
+  const float each = a.num_pairs > 0 ? 1.0f / static_cast<float>(a.num_pairs) : 0.0f;
+  const int32_t i = blockIdx.x;
+  if (i == a.num_docs) {
+    Pair loss = {0.0f, 0.0f};
+    bool bad = false;
+    for (int64_t p = threadIdx.x; p < a.num_pairs; p += kDocThreads) {
+      const int32_t c = a.chosen[p], r = a.rejected[p];
+      if (!pair_ok(a, c, r)) {
+        bad = true;
+        a.margins[p] = 0.0f;
+        continue;
+      }
+      const PairTerm t = pair_term(a, c, r);
+      a.margins[p] = t.h;
+      loss = add(loss, {t.loss, 0.0f});
+    }
+    if (bad) status_set(a.status, THD_ERR_INDEX_RANGE);
+    const float total = block_total_pair(loss, pairs);
+    if (threadIdx.x == 0) a.loss[0] = total * each;
+    return;
+  }
+  float ds = 0.0f;
+  for (int64_t p = threadIdx.x; p < a.num_pairs; p += kDocThreads) {
+    const int32_t c = a.chosen[p], r = a.rejected[p];
+    if ((c != i && r != i) || c == r || !pair_ok(a, c, r)) continue;
+    const float g = a.beta * each * pair_term(a, c, r).slope;
+    ds += c == i ? g : -g;
+  }
+  ds = block_total_pair({ds, 0.0f}, pairs);
+  if (a.length_normalized && a.count[i] > 0) ds /= static_cast<float>(a.count[i]);
+  const DocSlots d = doc_slots(a.cu, i, a.rows, m);
+  for (int32_t r = 0; r < m.cp; ++r) {
+    for (int64_t j = d.lo + threadIdx.x; j < d.hi; j += kDocThreads) {
+      const int64_t p = static_cast<int64_t>(r) * S + j;
+      a.dlogprobs[p] = a.mask[p] ? ds : 0.0f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// final sums
+// ---------------------------------------------------------------------------
+
+// out[k] = sum of a[k][t] * b[t], one block per k, the same order in every run.
+__global__ void __launch_bounds__(kSumThreads)
+    final_sums_kernel(const float* a, const float* b, int64_t n, float* out, const int32_t* st) {
+  pdl_wait_then_release();
+  __shared__ Pair pairs[32];
+  if (block_status_set(st)) return;
+  const float* v = a + blockIdx.x * n;
+  Pair sum = {0.0f, 0.0f};
+  for (int64_t t = threadIdx.x; t < n; t += kSumThreads) {
+    Pair x = {v[t], 0.0f};
+    if (b) {
+      const float w = b[t], y = x.hi;
+      // a row without weight takes no part, whatever its loss
+      x.hi = w == 0.0f ? 0.0f : y * w;
+      x.lo = fabsf(x.hi) < INFINITY ? fmaf(y, w, -x.hi) : 0.0f;
+      if (w == 0.0f) x.lo = 0.0f;
+    }
+    sum = add(sum, x);
+  }
+  const float total = block_total_pair(sum, pairs);
+  if (threadIdx.x == 0) out[blockIdx.x] = total;
+}
+
+thd_status_t done(cudaError_t e) {
+  if (e == cudaSuccess) return THD_OK;
+  record_cuda_error(e);
+  return THD_ERR_CUDA;
+}
+
+int32_t boundary_multiple(int32_t cp) { return cp == 1 ? 0 : 2 * cp; }
+
+}  // namespace
+
+thd_status_t launch_loss_weights(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t cp,
+                                 int32_t reduction, float* weights, int32_t* doc_ids, int32_t* counts, int32_t* status,
+                                 cudaStream_t s) {
+  const CpMath m = make_cp_math(cp);
+  const int32_t S = T / cp;
+  cudaError_t e = launch_pdl(count_rows_kernel, dim3(std::max(n, 1)), dim3(kDocThreads), 0, s, mask, cu, n, T, S, m,
+                             boundary_multiple(cp), counts, status);
+  if (e != cudaSuccess || T == 0) return done(e);
+  const int64_t blocks = (static_cast<int64_t>(T) + kDocThreads - 1) / kDocThreads;
+  const int grid = static_cast<int>(std::min<int64_t>(blocks, 8ll * sm_count()));
+  return done(launch_pdl(loss_weights_kernel, dim3(grid), dim3(kDocThreads), 0, s, mask, cu, n, T, S, m, reduction,
+                         static_cast<const int32_t*>(counts), weights, doc_ids, static_cast<const int32_t*>(status)));
+}
+
+thd_status_t launch_preference(const PreferenceArgs& a, cudaStream_t s) {
+  const CpMath m = make_cp_math(a.cp);
+  const int32_t S = a.rows / a.cp;
+  cudaError_t e = launch_pdl(doc_sums_kernel, dim3(std::max(a.num_docs, 1)), dim3(kDocThreads), 0, s, a, S, m,
+                             boundary_multiple(a.cp));
+  if (e != cudaSuccess) return done(e);
+  return done(launch_pdl(preference_kernel, dim3(a.num_docs + 1), dim3(kDocThreads), 0, s, a, S, m));
+}
+
+thd_status_t launch_final_sums(const float* a, const float* b, int32_t count, int64_t n, float* out, int32_t* status,
+                               cudaStream_t s) {
+  return done(launch_pdl(final_sums_kernel, dim3(count), dim3(kSumThreads), 0, s, a, b, n, out,
+                         static_cast<const int32_t*>(status)));
+}
+
+}  // namespace thd

@@ -1,0 +1,254 @@
+// Arguments of the loss kernels and the row arithmetic that all of them share
+// (not installed).
+#pragma once
+
+#include "logits.cuh"
+
+namespace thd {
+
+enum RowMode { ROW_SCORE = 0, ROW_POLICY = 1, ROW_DISTILL = 2 };
+
+// Teacher entries a row may have (thd_distill_topk_loss); the row's entries
+// are held in shared memory.
+constexpr int kMaxTeacher = THD_MAX_TEACHER_ENTRIES;
+
+struct RowArgs {
+  const void* logits;
+  int64_t stride;   // elements between rows
+  int32_t rows, vocab;
+  LogitScale scale;
+  int32_t* status;
+  const int32_t* labels;
+  const uint8_t* mask;     // ROW_SCORE
+  const float* weights;    // ROW_POLICY, ROW_DISTILL
+  // gradient (ROW_POLICY, ROW_DISTILL); null: no gradient
+  void* dlogits;
+  int64_t dstride;
+  float grad_scale;
+  // outputs
+  float* logprobs;  // ROW_SCORE, ROW_POLICY
+  float* lse;       // ROW_SCORE
+  float* terms;     // ROW_POLICY: [3][rows] w * (loss, kl, clipped)
+  float* token_losses;  // ROW_DISTILL
+  // ROW_POLICY
+  const float* old_logprobs;
+  const float* ref_logprobs;
+  const float* advantages;
+  const int32_t* doc_ids;
+  int32_t num_docs;
+  float ratio_min, ratio_max, kl_coef;
+  // ROW_DISTILL
+  const int32_t* teacher_ids;
+  const void* teacher_scores;
+  int32_t teacher_dtype, teacher_count, normalize;
+};
+
+// dz_v = k * exp((z_v - shift) / tau), and `at_label` in the label's place
+struct RowGrad {
+  float k, at_label;
+};
+
+// What one row needs besides its logits; read by one thread, before the row's
+// statistics are known.
+struct RowHead {
+  float weight;   // 0: the row takes no part
+  float z_label;
+  float old_lp, ref_lp, advantage;
+  int32_t label;
+};
+
+template <typename T, int kMode>
+__device__ __forceinline__ RowHead row_head(const RowArgs& a, int64_t t) {
+  RowHead h = {};
+  h.label = -1;
+  if (kMode == ROW_SCORE) h.weight = (!a.mask || a.mask[t]) ? 1.0f : 0.0f;
+  else h.weight = a.weights[t];
+  if (h.weight == 0.0f || kMode == ROW_DISTILL) return h;
+  h.label = a.labels[t];
+  bool ok = h.label >= 0 && h.label < a.vocab;
+  if (kMode == ROW_POLICY) {
+    int64_t at = t;
+    if (a.doc_ids) {
+      at = a.doc_ids[t];
+      ok = ok && at >= 0 && at < a.num_docs;
+    }
+    if (ok) h.advantage = a.advantages[at];
+    h.old_lp = a.old_logprobs[t];
+    if (a.ref_logprobs) h.ref_lp = a.ref_logprobs[t];
+  }
+  if (!ok) {  // reported, and the row takes no part
+    status_set(a.status, THD_ERR_INDEX_RANGE);
+    h.weight = 0.0f;
+    h.label = -1;
+    return h;
+  }
+  h.z_label = to_float(static_cast<const T*>(a.logits)[t * a.stride + h.label]);
+  return h;
+}
+
+// Scalar outputs of a row without weight.
+template <int kMode>
+__device__ __forceinline__ void write_idle_row(const RowArgs& a, int64_t t) {
+  if (kMode == ROW_SCORE || kMode == ROW_POLICY) a.logprobs[t] = 0.0f;
+  if (kMode == ROW_SCORE) a.lse[t] = 0.0f;
+  if (kMode == ROW_POLICY)
+    for (int k = 0; k < 3; ++k) a.terms[k * static_cast<int64_t>(a.rows) + t] = 0.0f;
+  if (kMode == ROW_DISTILL) a.token_losses[t] = 0.0f;
+}
+
+// Log-probability of the label; a row without any logit above -inf gives it
+// -inf (the quotient 0 / 0 of the formula has no value).
+__device__ __forceinline__ Pair label_logprob(float z, SoftmaxStat st, const RowNorm& r, LogitScale c) {
+  if (stat_is_empty(st) && z == -INFINITY) return {-INFINITY, 0.0f};
+  return log_prob(z, r, c);
+}
+
+__device__ __forceinline__ void write_score(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st) {
+  const RowNorm r = row_norm(st);
+  const Pair lp = label_logprob(h.z_label, st, r, a.scale);
+  a.logprobs[t] = lp.hi + lp.lo;
+  a.lse[t] = log_sum_exp(r, a.scale);
+}
+
+// Clipped policy loss of one row (formulas in include/thd.h) and the
+// coefficients of its gradient.  The ratio and the KL term take the
+// log-probability as a pair: its difference to old_lp and ref_lp is small,
+// and rounding it first would cost that difference about 5e-7.
+__device__ __forceinline__ RowGrad policy_row(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st,
+                                              bool write) {
+  const RowNorm r = row_norm(st);
+  const Pair lp = label_logprob(h.z_label, st, r, a.scale);
+  const float ratio = expf((lp.hi - h.old_lp) + lp.lo);
+  // comparisons, not min/max: a NaN ratio stays one
+  const float bounded = ratio < a.ratio_min ? a.ratio_min : (ratio > a.ratio_max ? a.ratio_max : ratio);
+  const float gain = ratio * h.advantage, bounded_gain = bounded * h.advantage;
+  const bool clipped = gain > bounded_gain;
+  float loss = -(clipped ? bounded_gain : gain), slope = clipped ? 0.0f : -gain, kl = 0.0f;
+  if (a.ref_logprobs) {
+    const float gap = (h.ref_lp - lp.hi) - lp.lo;
+    const float em1 = expm1f(gap);
+    kl = em1 - gap;
+    if (a.kl_coef != 0.0f) {
+      loss = fmaf(a.kl_coef, kl, loss);
+      slope = fmaf(-a.kl_coef, em1, slope);
+    }
+  }
+  if (write) {
+    const int64_t T = a.rows;
+    a.logprobs[t] = lp.hi + lp.lo;
+    a.terms[t] = h.weight * loss;
+    a.terms[T + t] = h.weight * kl;
+    a.terms[2 * T + t] = clipped ? h.weight : 0.0f;
+  }
+  // d loss / d z_v = w slope (1[v = label] - p_v) / tau
+  const float g = a.grad_scale * h.weight * slope * a.scale.inv_tau;
+  if (stat_is_empty(st)) return {0.0f, 0.0f};
+  return {-g / st.s, -g * expm1f(lp.hi)};
+}
+
+// ---------------------------------------------------------------------------
+// the row's teacher entries, in shared memory
+// ---------------------------------------------------------------------------
+
+struct Teacher {
+  int32_t id[kMaxTeacher];
+  float q[kMaxTeacher];    // probability; 0 for an absent entry
+  float lq[kMaxTeacher];   // logarithm of it
+  float mass;              // sum of q
+};
+
+__device__ __forceinline__ float teacher_score(const RowArgs& a, int64_t i) {
+  if (a.teacher_dtype == THD_DTYPE_BF16) return to_float(static_cast<const __nv_bfloat16*>(a.teacher_scores)[i]);
+  if (a.teacher_dtype == THD_DTYPE_F16) return to_float(static_cast<const __half*>(a.teacher_scores)[i]);
+  return static_cast<const float*>(a.teacher_scores)[i];
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+  return v;
+}
+
+// Filled by one whole warp; `report`: this caller tells of bad ids.
+__device__ __forceinline__ void load_teacher(const RowArgs& a, int64_t t, Teacher& s, bool report) {
+  const int lane = threadIdx.x & 31, K = a.teacher_count;
+  const int64_t base = t * K;
+  float top = -INFINITY;
+  bool bad = false;
+  for (int k = lane; k < K; k += 32) {
+    const int32_t id = a.teacher_ids[base + k];
+    float v = teacher_score(a, base + k);
+    bad |= id >= a.vocab;
+    const bool here = id >= 0 && id < a.vocab;
+    s.id[k] = here ? id : -1;
+    if (!here) v = -INFINITY;
+    s.lq[k] = v;
+    top = fmaxf(top, v);
+  }
+  if (bad && report) status_set(a.status, THD_ERR_INDEX_RANGE);
+  float norm = 0.0f;
+  if (a.normalize) {
+    top = softmax_shift(warp_max(top));
+    float sum = 0.0f;
+    for (int k = lane; k < K; k += 32) sum += exp_scaled(s.lq[k] - top, a.scale);
+    sum = warp_sum(sum);
+    // without any entry every score stays -inf
+    norm = sum == 0.0f ? 0.0f : logf(sum);
+  }
+  float mass = 0.0f;
+  for (int k = lane; k < K; k += 32) {
+    float v = s.lq[k];
+    if (a.normalize) v = (v - top) / a.scale.tau - norm;
+    const float q = expf(v);
+    s.lq[k] = v;
+    s.q[k] = q;
+    mass += q;
+  }
+  mass = warp_sum(mass);
+  if (lane == 0) s.mass = mass;
+}
+
+// The student's log-probability of an entry; `empty`: no logit of the row is
+// above -inf
+__device__ __forceinline__ Pair entry_logprob(float z, bool empty, const RowNorm& r, LogitScale c) {
+  return empty ? Pair{-INFINITY, 0.0f} : log_prob(z, r, c);
+}
+
+// launchers
+thd_status_t launch_row_loss(RowMode mode, int32_t dtype, const RowArgs& a, cudaStream_t s);
+thd_status_t launch_logprobs_backward(int32_t dtype, const RowArgs& a, const float* lse, const float* dlogprobs,
+                                      cudaStream_t s);
+// out[k] = sum over t of a[k][t] (* b[t] when given), k < count, in a fixed order
+thd_status_t launch_final_sums(const float* a, const float* b, int32_t count, int64_t n, float* out, int32_t* status,
+                               cudaStream_t s);
+thd_status_t launch_loss_weights(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t cp,
+                                 int32_t reduction, float* weights, int32_t* doc_ids, int32_t* counts, int32_t* status,
+                                 cudaStream_t s);
+
+struct PreferenceArgs {
+  const float* logprobs;
+  const float* ref_logprobs;
+  const uint8_t* mask;
+  const int32_t* cu;
+  int32_t num_docs, rows, cp;
+  const int32_t* chosen;
+  const int32_t* rejected;
+  int32_t num_pairs;
+  float beta, smoothing, margin;
+  int32_t length_normalized;
+  float* loss;
+  float* margins;
+  float* doc_logprobs;
+  float* dlogprobs;
+  float* gain;     // workspace [num_docs]: sum (or mean) of lp - ref
+  int32_t* count;  // workspace [num_docs]: rows with loss
+  int32_t* status;
+};
+thd_status_t launch_preference(const PreferenceArgs& a, cudaStream_t s);
+
+}  // namespace thd

@@ -417,6 +417,225 @@ thd_status_t thd_pack_docs_noalloc(const int32_t *raw, int32_t B, int64_t S, int
                                    int64_t docs_capacity, int64_t *counts, int32_t *d_status,
                                    cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Losses of a packed batch
+ *
+ * What a training step computes from the batch the calls above lay out: T
+ * rows of logits over a vocabulary of V, their labels and loss mask
+ * (thd_roll_labels, or in the zigzag layout thd_roll_labels_zigzag) and the
+ * padded document boundaries.  With z the logits, tau the temperature, y the
+ * labels:
+ *   lse[t]  = ln sum_v exp(z[t][v] / tau)
+ *   lp[t]   = z[t][y[t]] / tau - lse[t]
+ *   p[t][v] = exp(z[t][v] / tau - lse[t])
+ * Sums, maxima and all row scalars are held in 32 bits or more whatever the
+ * logits' type; gradients are rounded once to the type of the logits.  Every
+ * result is the same bits from run to run (no floating-point atomics).
+ *
+ * A row without loss (mask 0, weight 0, incoming gradient 0) takes no part:
+ * its logits are not read (whatever they hold), its scalar results are 0 and
+ * its row of the gradient is zeros.  A row of which no logit is above -inf has
+ * lse = -inf, lp = -inf and a zero gradient.  A label outside [0, V) of a row
+ * that has loss is reported as THD_ERR_INDEX_RANGE and its row takes no part.
+ * d_status may be NULL in these calls: bad data is then skipped unreported.
+ * ------------------------------------------------------------------------ */
+
+typedef enum thd_dtype {
+  THD_DTYPE_F32 = 0,
+  THD_DTYPE_BF16 = 1,
+  THD_DTYPE_F16 = 2
+} thd_dtype_t;
+
+/* Logits: device [rows][row_stride] elements, of which a row's first `vocab`
+ * count (a vocabulary padded for alignment has row_stride > vocab).  Any
+ * element-aligned address and stride; 16-byte aligned rows are not required
+ * for speed, but see thd_gradient_t.
+ *  dtype        thd_dtype_t
+ *  vocab        1 .. 2^31 - 1
+ *  temperature  1e-4 .. 1e4 */
+typedef struct thd_logits {
+  const void *data;
+  int64_t rows;
+  int64_t row_stride;
+  int32_t vocab;
+  int32_t dtype;
+  float temperature;
+  int32_t reserved; /* 0 */
+} thd_logits_t;
+
+/* The logits' gradient: device [rows][row_stride], the logits' type; each
+ * row's first `vocab` elements are written, nothing else.  It may be the
+ * logits themselves (same address and stride: the gradient replaces them);
+ * otherwise the two must not overlap.
+ *  scale  factor of the gradient only (a loss scale; 1 for none). */
+typedef struct thd_gradient {
+  void *dlogits;
+  int64_t row_stride;
+  float scale;
+  int32_t reserved; /* 0 */
+} thd_gradient_t;
+
+typedef enum thd_reduction {
+  THD_TOKEN_MEAN = 0, /* every row with loss counts the same */
+  THD_DOC_MEAN = 1,   /* every document with a row with loss counts the same */
+  THD_TOKEN_SUM = 2   /* weight 1 */
+} thd_reduction_t;
+
+/*
+ * Weights of the rows in a loss that is their weighted sum, and the document
+ * of each row.  With m the mask, n_i the rows of document i with m != 0:
+ *   THD_TOKEN_MEAN  w = m / sum_i n_i
+ *   THD_DOC_MEAN    w = m / (n_i * D), D = documents with n_i > 0
+ *   THD_TOKEN_SUM   w = m
+ * so the weights of a mean add up to 1, or are all 0 when no row has loss.
+ * Rows are those of the zigzag layout of cp_size ranks; the contiguous layout
+ * is cp_size = 1 (documents of any length then).
+ *  loss_mask   device uint8[T]
+ *  weights     device float[T]
+ *  doc_ids     device int32[T] or NULL
+ *  workspace   device, >= thd_loss_weights_workspace_bytes(num_docs), 4-byte aligned
+ * Device checks of the boundaries as for thd_route_build (the divisibility
+ * check when cp_size > 1).
+ */
+size_t thd_loss_weights_workspace_bytes(int32_t num_docs);
+thd_status_t thd_loss_weights(const uint8_t *loss_mask, const int32_t *cu_seqlens_padded, int32_t num_docs,
+                              int64_t T, int32_t cp_size, int32_t reduction, float *weights, int32_t *doc_ids,
+                              void *workspace, size_t workspace_bytes, int32_t *d_status,
+                              cudaStream_t stream);
+
+/*
+ * Log-probabilities of the labels: logprobs[t] = lp[t], lse[t] as above.
+ *  labels     device int32[rows]
+ *  loss_mask  device uint8[rows], or NULL: every row takes part
+ */
+thd_status_t thd_token_logprobs(const thd_logits_t *logits, const int32_t *labels, const uint8_t *loss_mask,
+                                float *logprobs, float *lse, int32_t *d_status, cudaStream_t stream);
+
+/*
+ * Its gradient: with g[t] = dlogprobs[t],
+ *   dlogits[t][v] = scale * g[t] * (1[v = y[t]] - p[t][v]) / tau.
+ *  lse  what thd_token_logprobs wrote for the same logits
+ */
+thd_status_t thd_token_logprobs_backward(const thd_logits_t *logits, const int32_t *labels, const float *lse,
+                                         const float *dlogprobs, const thd_gradient_t *gradient,
+                                         int32_t *d_status, cudaStream_t stream);
+
+/*
+ * Clipped policy loss with a KL term, its gradient in the same pass over the
+ * logits.  With A the advantage, r = exp(lp - old), d = ref - lp:
+ *   pg = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *   kl = exp(d) - d - 1                    (0 without a reference)
+ *   sums[0] = sum_t w[t] (pg + kl_coef kl)               the loss
+ *   sums[1] = sum_t w[t] kl
+ *   sums[2] = sum_t w[t] [r A > clip(r) A]               share clipped
+ *   dlogits[t][v] = scale * w[t] dl/dlp (1[v = y] - p[v]) / tau,
+ *   dl/dlp = -r A where r A <= clip(r) A, else 0;  + kl_coef (1 - exp(d))
+ *  weights        device float[rows]
+ *  logprobs       device float[rows]: lp
+ *  gradient       NULL: the loss alone
+ *  sums           device float[3]
+ *  workspace      device, >= thd_policy_loss_workspace_bytes(rows), 4-byte aligned
+ * Fields of thd_policy_t:
+ *  old_logprobs   device float[rows]
+ *  ref_logprobs   device float[rows] or NULL
+ *  advantages     device float[rows]; or float[num_docs] with doc_ids given
+ *  doc_ids        device int32[rows] (thd_loss_weights) or NULL; an id outside
+ *                 [0, num_docs) of a row with weight is THD_ERR_INDEX_RANGE
+ *  clip_low       0 .. 1;  clip_high >= 0;  kl_coef finite
+ */
+typedef struct thd_policy {
+  const float *old_logprobs;
+  const float *ref_logprobs;
+  const float *advantages;
+  const int32_t *doc_ids;
+  int32_t num_docs;
+  float clip_low;
+  float clip_high;
+  float kl_coef;
+} thd_policy_t;
+
+size_t thd_policy_loss_workspace_bytes(int64_t rows);
+thd_status_t thd_policy_loss(const thd_logits_t *logits, const int32_t *labels, const float *weights,
+                             const thd_policy_t *policy, const thd_gradient_t *gradient, float *logprobs,
+                             float *sums, void *workspace, size_t workspace_bytes, int32_t *d_status,
+                             cudaStream_t stream);
+
+/*
+ * Preference loss over pairs of documents of the batch.  With m the mask and
+ * s_i = sum over the rows of document i with m != 0 of lp, u_i the same sum of
+ * lp - ref (both divided by the number of those rows when length_normalized):
+ *   h_p  = beta (u[chosen[p]] - u[rejected[p]])
+ *   loss = mean_p -(1 - eps) ln sigmoid(h_p - margin) - eps ln sigmoid(margin - h_p)
+ *   dlogprobs = d loss / d lp
+ * and thd_token_logprobs_backward carries dlogprobs on to the logits.  A
+ * document may be in any number of pairs.
+ *  logprobs, ref_logprobs  device float[T]; ref_logprobs NULL: no reference.
+ *                          Rows with m = 0 are not read.
+ *  loss_mask          device uint8[T]
+ *  cp_size            layout of the rows, as in thd_loss_weights
+ *  chosen, rejected   device int32[num_pairs], documents; one outside
+ *                     [0, num_docs) is THD_ERR_INDEX_RANGE and its pair adds
+ *                     nothing (margin 0).  num_pairs = 0: loss 0.
+ *  loss               device float[1]
+ *  margins            device float[num_pairs]: h_p
+ *  doc_logprobs       device float[num_docs]: s_i
+ *  dlogprobs          device float[T]
+ *  workspace          device, >= thd_preference_loss_workspace_bytes(num_docs), 4-byte aligned
+ *  params             label_smoothing eps 0 .. 1; beta, margin finite
+ */
+typedef struct thd_preference {
+  const float *ref_logprobs;
+  float beta;
+  float label_smoothing;
+  float margin;
+  int32_t length_normalized;
+} thd_preference_t;
+
+size_t thd_preference_loss_workspace_bytes(int32_t num_docs);
+thd_status_t thd_preference_loss(const float *logprobs, const uint8_t *loss_mask, const int32_t *cu_seqlens_padded,
+                                 int32_t num_docs, int64_t T, int32_t cp_size, const int32_t *chosen,
+                                 const int32_t *rejected, int32_t num_pairs, const thd_preference_t *params,
+                                 float *loss, float *margins, float *doc_logprobs, float *dlogprobs,
+                                 void *workspace, size_t workspace_bytes, int32_t *d_status,
+                                 cudaStream_t stream);
+
+/*
+ * Distillation from the entries a teacher kept of each row, its gradient in
+ * the same pass over the logits.  Row t has `count` entries (id, score); those
+ * with id < 0 are absent.  q over the entries that are there:
+ *   normalize   scores are logits: q_k = softmax(score / tau)
+ *   otherwise   scores are log-probabilities: q_k = exp(score_k) (their sum
+ *               Q may be below 1; the teacher's rest counts nothing)
+ *   token_losses[t] = tau^2 sum_k q_k (ln q_k - lp(id_k))
+ *   loss            = sum_t w[t] token_losses[t]
+ *   dlogits[t][v]   = scale * w[t] tau (Q p[v] - sum_{k: id_k = v} q_k)
+ * where lp(v) is the row's log-probability of v.  An entry with q = 0 (score
+ * -inf) adds nothing; a row without entries has loss and gradient 0; an id
+ * may come more than once.  An id >= V of a row with weight is
+ * THD_ERR_INDEX_RANGE and counts as absent.
+ *  weights        device float[rows]
+ *  token_losses   device float[rows]
+ *  loss           device float[1]
+ *  gradient       NULL: the loss alone
+ * Fields of thd_teacher_t:
+ *  ids            device int32[rows][count]
+ *  scores         device [rows][count] of dtype (thd_dtype_t)
+ *  count          1 .. THD_MAX_TEACHER_ENTRIES
+ */
+#define THD_MAX_TEACHER_ENTRIES 1024
+typedef struct thd_teacher {
+  const int32_t *ids;
+  const void *scores;
+  int32_t count;
+  int32_t dtype;
+  int32_t normalize;
+  int32_t reserved; /* 0 */
+} thd_teacher_t;
+
+thd_status_t thd_distill_topk_loss(const thd_logits_t *logits, const thd_teacher_t *teacher, const float *weights,
+                                   const thd_gradient_t *gradient, float *token_losses, float *loss,
+                                   int32_t *d_status, cudaStream_t stream);
+
 /* Status word helpers.  thd_status_clear enqueues a zero write.
  * thd_status_read copies the word to *host_code and synchronises `stream`:
  * the one call of this library that waits for the GPU. */

@@ -12,3 +12,4 @@ from .thd_oracle import (  # noqa: F401
     validate_label_args, roll_labels, roll_labels_zigzag, pack_docs,
     SEQ_TO_HEAD, HEAD_TO_SEQ, ulysses_swap,
 )
+from . import losses  # noqa: F401
