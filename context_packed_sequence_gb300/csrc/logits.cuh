@@ -12,10 +12,12 @@
 
 namespace thd {
 
-// log2(e) / temperature as the sum of two floats.  hi is rounded towards zero,
-// so lo > 0 and d*hi + d*lo never mixes infinities of both signs.  A softmax
-// scaled by hi alone is the softmax of a temperature up to 6e-8 off: the same
-// error in every row, which sums of log-probabilities over a document add up.
+// What a logit is multiplied by: inv_tau, the reciprocal of the temperature in
+// 32 bits, and in the kernels' exponents log2(e) * inv_tau as the sum of two
+// floats.  hi is rounded towards zero, so lo > 0 and d*hi + d*lo never mixes
+// infinities of both signs.  A softmax scaled by hi alone is that of a
+// temperature up to 6e-8 off: the same error in every row, which sums of
+// log-probabilities over a document add up.
 struct LogitScale {
   float hi, lo;
   float tau, inv_tau;
@@ -23,12 +25,12 @@ struct LogitScale {
 
 inline LogitScale make_logit_scale(float temperature) {
   LogitScale s;
-  const double c = 1.4426950408889634 / static_cast<double>(temperature);
+  s.tau = temperature;
+  s.inv_tau = 1.0f / temperature;
+  const double c = 1.4426950408889634 * static_cast<double>(s.inv_tau);
   s.hi = static_cast<float>(c);
   if (static_cast<double>(s.hi) >= c) s.hi = std::nextafterf(s.hi, 0.0f);
   s.lo = static_cast<float>(c - static_cast<double>(s.hi));
-  s.tau = temperature;
-  s.inv_tau = static_cast<float>(1.0 / static_cast<double>(temperature));
   return s;
 }
 
@@ -38,7 +40,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 2^(d * log2(e) / temperature) = exp(d / temperature)
+// 2^(d * log2(e) * inv_tau) = exp(d * inv_tau)
 __device__ __forceinline__ float exp_scaled(float d, LogitScale c) { return ex2(fmaf(d, c.hi, d * c.lo)); }
 
 // ---------------------------------------------------------------------------
@@ -62,47 +64,6 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
-
-// ---------------------------------------------------------------------------
-// softmax statistics
-// ---------------------------------------------------------------------------
-
-// Running maximum m of some logits and the sum s of exp((z - shift(m)) / tau).
-// The shift is m itself, or 0 while m is not finite: a set whose logits are
-// all -inf then has s = 0, one that holds +inf has s = +inf, and a NaN makes
-// s NaN, without a case of its own.
-struct SoftmaxStat {
-  float m, s;
-};
-
-__device__ __forceinline__ float softmax_shift(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
-
-__device__ __forceinline__ SoftmaxStat empty_stat() { return {-INFINITY, 0.0f}; }
-
-// s of a set with maximum m, rescaled to the shift of the larger maximum `to`
-__device__ __forceinline__ float rescaled(float m, float s, float to, LogitScale c) {
-  if (m == to || s == 0.0f) return s;
-  return s * exp_scaled(softmax_shift(m) - softmax_shift(to), c);
-}
-
-__device__ __forceinline__ SoftmaxStat join(SoftmaxStat a, SoftmaxStat b, LogitScale c) {
-  const float m = fmaxf(a.m, b.m);
-  return {m, rescaled(a.m, a.s, m, c) + rescaled(b.m, b.s, m, c)};
-}
-
-// A row none of whose logits is above -inf: its probabilities are taken as 0.
-__device__ __forceinline__ bool stat_is_empty(SoftmaxStat t) { return t.m == -INFINITY && t.s == 0.0f; }
-
-__device__ __forceinline__ SoftmaxStat warp_join(SoftmaxStat t, LogitScale c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    SoftmaxStat u;
-    u.m = __shfl_xor_sync(kFullMask, t.m, o);
-    u.s = __shfl_xor_sync(kFullMask, t.s, o);
-    t = join(t, u, c);
-  }
-  return t;
-}
 
 // ---------------------------------------------------------------------------
 // float pairs: an unevaluated sum hi + lo with |lo| at most an ulp of hi
@@ -136,9 +97,10 @@ __device__ __forceinline__ Pair scaled(Pair p, float k_hi, float k_lo) {
 constexpr float kLn2Hi = 0.693147182464599609375f;  // ln 2 rounded to a float
 constexpr float kLn2Lo = -1.904654299957767e-9f;    // ln 2 - kLn2Hi
 
-// log2(s) as a whole number plus the logarithm of a number near 1, whose
-// error is relative to itself
-__device__ __forceinline__ Pair log2_pair(float s) {
+// log2 of a sum as a whole number plus the logarithm of a number near 1, whose
+// error is relative to itself; the pair's low part enters to first order
+__device__ __forceinline__ Pair log2_pair(Pair sum) {
+  const float s = sum.hi;
   if (!(s >= 1.17549435e-38f && s < INFINITY)) return {log2f(s), 0.0f};
   int32_t bits = __float_as_int(s);
   int32_t ex = (bits >> 23) - 127;
@@ -147,8 +109,54 @@ __device__ __forceinline__ Pair log2_pair(float s) {
     f *= 0.5f;
     ++ex;
   }
-  return two_sum(static_cast<float>(ex), log2f(f));
+  const Pair l = two_sum(static_cast<float>(ex), log2f(f));
+  return {l.hi, l.lo + sum.lo / s * 1.44269504f};  // log2(hi + lo) = log2(hi) + lo / (hi ln 2)
 }
+
+// ---------------------------------------------------------------------------
+// softmax statistics
+// ---------------------------------------------------------------------------
+
+// ex2.approx on GB300 is low by this share of its value on average (4 M
+// arguments spread over [-24, 0]: mean -5.1e-8, at most 1.4e-7 off; 2^0 is
+// exactly 1).  A sum of many exponentials inherits the mean in full, and a sum
+// of log-probabilities over a document would add it up.
+constexpr float kEx2Bias = 5.1e-8f;
+
+// Running maximum m of some logits and the sum s of exp((z - shift(m)) / tau).
+// The shift is m itself, or 0 while m is not finite: a set whose logits are
+// all -inf then has s = 0, one that holds +inf has s = +inf, and a NaN makes
+// s NaN, without a case of its own.
+struct SoftmaxStat {
+  float m;
+  Pair s;
+};
+
+__device__ __forceinline__ float softmax_shift(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+
+__device__ __forceinline__ SoftmaxStat empty_stat() { return {-INFINITY, {0.0f, 0.0f}}; }
+
+// The sum of a set with maximum m, rescaled to the shift of the larger maximum
+// `to`.  One factor scales a whole partial sum, so the rounding of its
+// exponent and the mean error of ex2 go into the low part.
+__device__ __forceinline__ Pair rescaled(float m, Pair s, float to, LogitScale c) {
+  if (m == to || s.hi == 0.0f) return s;
+  const float d = softmax_shift(m) - softmax_shift(to);
+  const float x = d * c.hi;
+  const float f = ex2(x);
+  const float rest = fmaf(d, c.hi, -x) + d * c.lo;
+  const float hi = s.hi * f;
+  const float lo = fmaf(s.hi, f, -hi) + hi * fmaf(rest, 0.693147181f, kEx2Bias) + s.lo * f;
+  return {hi, f > 0.0f && fabsf(hi) < INFINITY ? lo : 0.0f};
+}
+
+// A set's own sum of n exponentials, one of them the maximum's (exactly 1)
+__device__ __forceinline__ Pair unbiased_sum(float s) {
+  return {s, s > 1.0f && s < INFINITY ? (s - 1.0f) * kEx2Bias : 0.0f};
+}
+
+// A row none of whose logits is above -inf: its probabilities are taken as 0.
+__device__ __forceinline__ bool stat_is_empty(SoftmaxStat t) { return t.m == -INFINITY && t.s.hi == 0.0f; }
 
 // A row's log of its sum (relative to the shift), kept for its scalars.
 struct RowNorm {
@@ -160,21 +168,14 @@ __device__ __forceinline__ RowNorm row_norm(SoftmaxStat t) {
   return {softmax_shift(t.m), scaled(log2_pair(t.s), kLn2Hi, kLn2Lo)};
 }
 
-// x / tau for a pair x
-__device__ __forceinline__ Pair over_tau(Pair x, LogitScale c) {
-  const float q = x.hi / c.tau;
-  const float e = (fmaf(-q, c.tau, x.hi) + x.lo) * c.inv_tau;
-  return {q, fabsf(q) < INFINITY ? e : 0.0f};
-}
-
 // Logarithm of the probability of a logit z, as a pair.  Its error is that of
 // the sum: the large numbers z and m are subtracted before anything is rounded.
 __device__ __forceinline__ Pair log_prob(float z, const RowNorm& r, LogitScale c) {
-  return add(over_tau(two_sum(z, -r.shift), c), {-r.log_sum.hi, -r.log_sum.lo});
+  return add(scaled(two_sum(z, -r.shift), c.inv_tau, 0.0f), {-r.log_sum.hi, -r.log_sum.lo});
 }
 
 __device__ __forceinline__ float log_sum_exp(const RowNorm& r, LogitScale c) {
-  const Pair n = add(over_tau({r.shift, 0.0f}, c), r.log_sum);
+  const Pair n = add(scaled({r.shift, 0.0f}, c.inv_tau, 0.0f), r.log_sum);
   return n.hi + n.lo;
 }
 

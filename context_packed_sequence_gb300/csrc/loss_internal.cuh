@@ -143,19 +143,28 @@ __device__ __forceinline__ RowGrad policy_row(const RowArgs& a, int64_t t, const
   // d loss / d z_v = w slope (1[v = label] - p_v) / tau
   const float g = a.grad_scale * h.weight * slope * a.scale.inv_tau;
   if (stat_is_empty(st)) return {0.0f, 0.0f};
-  return {-g / st.s, -g * expm1f(lp.hi)};
+  return {-g / st.s.hi, -g * expm1f(lp.hi)};
 }
 
 // ---------------------------------------------------------------------------
 // the row's teacher entries, in shared memory
 // ---------------------------------------------------------------------------
 
+// Arrays of teacher_count entries, rounded up to a multiple of 4.
 struct Teacher {
-  int32_t id[kMaxTeacher];
-  float q[kMaxTeacher];    // probability; 0 for an absent entry
-  float lq[kMaxTeacher];   // logarithm of it
-  float mass;              // sum of q
+  int32_t* id;  // -1: absent
+  float* q;     // probability; 0 for an absent entry
+  float* lq;    // logarithm of it
 };
+
+__host__ __device__ __forceinline__ int32_t teacher_slots(int32_t count) { return (count + 3) & ~3; }
+__host__ __device__ __forceinline__ size_t teacher_bytes(int32_t count) {
+  return 3 * sizeof(float) * static_cast<size_t>(teacher_slots(count));
+}
+__device__ __forceinline__ Teacher teacher_at(void* mem, int32_t count) {
+  const int32_t n = teacher_slots(count);
+  return {static_cast<int32_t*>(mem), static_cast<float*>(mem) + n, static_cast<float*>(mem) + 2 * n};
+}
 
 __device__ __forceinline__ float teacher_score(const RowArgs& a, int64_t i) {
   if (a.teacher_dtype == THD_DTYPE_BF16) return to_float(static_cast<const __nv_bfloat16*>(a.teacher_scores)[i]);
@@ -174,8 +183,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Filled by one whole warp; `report`: this caller tells of bad ids.
-__device__ __forceinline__ void load_teacher(const RowArgs& a, int64_t t, Teacher& s, bool report) {
+// Filled by one whole warp; `report`: this caller tells of bad ids.  Returns
+// the sum of the probabilities.
+__device__ __forceinline__ float load_teacher(const RowArgs& a, int64_t t, const Teacher& s, bool report) {
   const int lane = threadIdx.x & 31, K = a.teacher_count;
   const int64_t base = t * K;
   float top = -INFINITY;
@@ -203,14 +213,32 @@ __device__ __forceinline__ void load_teacher(const RowArgs& a, int64_t t, Teache
   float mass = 0.0f;
   for (int k = lane; k < K; k += 32) {
     float v = s.lq[k];
-    if (a.normalize) v = (v - top) / a.scale.tau - norm;
+    if (a.normalize) v = (v - top) * a.scale.inv_tau - norm;
     const float q = expf(v);
     s.lq[k] = v;
     s.q[k] = q;
     mass += q;
   }
-  mass = warp_sum(mass);
-  if (lane == 0) s.mass = mass;
+  for (int k = K + lane; k < teacher_slots(K); k += 32) {
+    s.id[k] = -1;
+    s.q[k] = 0.0f;
+  }
+  return warp_sum(mass);
+}
+
+// Sum of the probabilities of the entries with this id (an id may come more
+// than once), four entries a step.
+__device__ __forceinline__ float entry_mass(const Teacher& s, int32_t id, int32_t count) {
+  float q = 0.0f;
+  for (int32_t i = 0; i < teacher_slots(count); i += 4) {
+    const int4 d = *reinterpret_cast<const int4*>(s.id + i);
+    const float4 v = *reinterpret_cast<const float4*>(s.q + i);
+    q += d.x == id ? v.x : 0.0f;
+    q += d.y == id ? v.y : 0.0f;
+    q += d.z == id ? v.z : 0.0f;
+    q += d.w == id ? v.w : 0.0f;
+  }
+  return q;
 }
 
 // The student's log-probability of an entry; `empty`: no logit of the row is

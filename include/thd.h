@@ -423,8 +423,8 @@ thd_status_t thd_pack_docs_noalloc(const int32_t *raw, int32_t B, int64_t S, int
  * What a training step computes from the batch the calls above lay out: T
  * rows of logits over a vocabulary of V, their labels and loss mask
  * (thd_roll_labels, or in the zigzag layout thd_roll_labels_zigzag) and the
- * padded document boundaries.  With z the logits, tau the temperature, y the
- * labels:
+ * padded document boundaries.  With z the logits, tau the temperature (a
+ * logit is multiplied by 1 / tau, rounded to 32 bits), y the labels:
  *   lse[t]  = ln sum_v exp(z[t][v] / tau)
  *   lp[t]   = z[t][y[t]] / tau - lse[t]
  *   p[t][v] = exp(z[t][v] / tau - lse[t])
