@@ -777,39 +777,111 @@ thd_status_t launch_type(RowMode mode, const RowArgs& a, cudaStream_t s) {
   return launch_mode<T, ROW_DISTILL>(a, s);
 }
 
-// dz_v = g_t (1[v = label] - p_v) / tau from the saved log-sum-exp
+// ---------------------------------------------------------------------------
+// gradient from saved log-sum-exps
+// ---------------------------------------------------------------------------
+
+constexpr int kBackThreads = 256;
+constexpr int kBackTile = 2 * kBackThreads * kVecsPerStep;  // vectors of a block
+
+// dz_v = g_t (1[v = label] - p_v) / tau, elementwise: a block takes one tile of
+// one row.  Rows go from the last to the first, since those that the forward
+// pass read last are still in the L2.  No barriers: every thread reads the
+// row's scalars itself.
 template <typename T>
-__global__ void __launch_bounds__(kPlainThreads)
-    logprobs_backward_kernel(const __grid_constant__ RowArgs a, const float* lse, const float* dlogprobs) {
+__global__ void __launch_bounds__(kBackThreads)
+    logprobs_backward_kernel(const __grid_constant__ RowArgs a, const float* lse, const float* dlogprobs, int32_t tiles) {
+  constexpr int N = Word<T>::kElems;
+  constexpr int kStep = kBackThreads * kVecsPerStep;
   pdl_wait_then_release();
-  __shared__ int32_t stop;
-  const int64_t t = blockIdx.x;
-  const uint32_t V = a.vocab, step = blockDim.x;
+  const int tid = threadIdx.x;
+  const uint32_t from_last = blockIdx.x / static_cast<uint32_t>(tiles);
+  const int64_t t = a.rows - 1 - static_cast<int32_t>(from_last);
+  const int32_t tile = static_cast<int32_t>(blockIdx.x - from_last * tiles);
   const int32_t label = a.labels[t];
-  const float up = dlogprobs[t];
-  const bool bad = up != 0.0f && (label < 0 || label >= a.vocab);
-  if (threadIdx.x == 0) {
-    stop = status_load(a.status);
-    if (bad && !stop) status_set(a.status, THD_ERR_INDEX_RANGE);
-  }
-  __syncthreads();
-  if (stop) return;
+  const float up = dlogprobs[t], l = lse[t];
+  if (status_load(a.status) != 0) return;
   const T* z = static_cast<const T*>(a.logits) + t * a.stride;
   T* dz = static_cast<T*>(a.dlogits) + t * a.dstride;
-  const float l = lse[t];
-  if (up == 0.0f || bad || l == -INFINITY) {
-    for (uint32_t v = threadIdx.x; v < V; v += step) dz[v] = from_float<T>(0.0f);
-    return;
-  }
+  const Slice row = row_slice(z, a.vocab, 0, 0);
+  const int32_t first = tile * kBackTile, count = min(kBackTile, row.count - first);
+  const int32_t lo_v = row.head + first * N, hi_v = lo_v + max(count, 0) * N;
+  const bool bad = up != 0.0f && (label < 0 || label >= a.vocab);
+  if (bad && tid == 0) status_set(a.status, THD_ERR_INDEX_RANGE);
+  // a row that takes no part: zeros, and its logits are not read
+  const bool idle = up == 0.0f || bad || l == -INFINITY;
   const float g = up * a.grad_scale * a.scale.inv_tau;
   // z/tau - lse = (z - top)/tau; what lse tau rounds off goes into the factor
   const float top = l * a.scale.tau;
   const float rest = fabsf(top) < INFINITY ? fmaf(-top, a.scale.inv_tau, l) : 0.0f;
-  const float k = g * ex2(-rest * 1.44269504f);
-  for (uint32_t v = threadIdx.x; v < V; v += step) {
-    const float d = k * exp_scaled(to_float(z[v]) - top, a.scale);
-    dz[v] = from_float<T>(static_cast<int32_t>(v) == label ? g - d : -d);
+  const float k = -g * ex2(-rest * 1.44269504f);
+  // the label's element is written again by the thread that wrote it, from
+  // the logit read before
+  int32_t writer = -1;
+  if (!idle) {
+    if (label >= lo_v && label < hi_v) writer = (label - lo_v) / N % kBackThreads;
+    else if (tile == 0 && label < row.head) writer = label;
+    else if (tile == 0 && label >= row.head + row.count * N) writer = row.edge_count - (a.vocab - label);
   }
+  const float z_label = tid == writer ? to_float(z[label]) : 0.0f;
+
+  const uint64_t neg = pack2(-top, -top), hi = pack2(a.scale.hi, a.scale.hi), k2 = pack2(k, k);
+  const auto gradient = [&](const uint4& v) {
+    uint4 d;
+#pragma unroll
+    for (int j = 0; j < Word<T>::kPairs; ++j)
+      Word<T>::set_pair(d, j, mul2(k2, ex2_2(mul2(add2(Word<T>::pair(v, j), neg), hi))));
+    return d;
+  };
+  const uint4 zeros = make_uint4(0, 0, 0, 0);
+  T* dv = dz + lo_v;
+  if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+    const uint4* from = reinterpret_cast<const uint4*>(z + lo_v) + tid;
+    uint4* to = reinterpret_cast<uint4*>(dv) + tid;
+    int32_t left = count - tid;
+    for (; left > kStep - kBackThreads; left -= kStep, from += kStep, to += kStep) {
+      uint4 v[kVecsPerStep];
+#pragma unroll
+      for (int u = 0; u < kVecsPerStep; ++u) v[u] = idle ? zeros : from[u * kBackThreads];
+#pragma unroll
+      for (int u = 0; u < kVecsPerStep; ++u) to[u * kBackThreads] = idle ? zeros : gradient(v[u]);
+    }
+    for (; left > 0; left -= kBackThreads, from += kBackThreads, to += kBackThreads)
+      *to = idle ? zeros : gradient(*from);
+  } else {
+    // a gradient laid out to another alignment than the logits
+    const uint4* from = reinterpret_cast<const uint4*>(z + lo_v);
+    for (int32_t i = tid; i < count; i += kBackThreads) {
+      const uint4 d = idle ? zeros : gradient(from[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + j, d, j);
+    }
+  }
+  if (tile == 0 && tid < row.edge_count) {
+    const int32_t e = edge_index(row, tid, a.vocab);
+    dz[e] = from_float<T>(idle ? 0.0f : k * ex2((to_float(z[e]) - top) * a.scale.hi));
+  }
+  if (tid == writer) dz[label] = from_float<T>(g + k * exp_scaled(z_label - top, a.scale));
+}
+
+template <typename T>
+thd_status_t launch_backward(const RowArgs& a, const float* lse, const float* dlogprobs, cudaStream_t s) {
+  const int64_t vecs = static_cast<int64_t>(a.vocab) * sizeof(T) / 16;
+  const int64_t tiles = std::max<int64_t>(1, (vecs + kBackTile - 1) / kBackTile);
+  // a grid has at most 2^31 - 1 blocks: rows in parts
+  const int64_t most = std::max<int64_t>(1, INT32_MAX / tiles);
+  for (int64_t done_rows = 0; done_rows < a.rows; done_rows += most) {
+    RowArgs part = a;
+    part.rows = static_cast<int32_t>(std::min(most, a.rows - done_rows));
+    part.labels = a.labels + done_rows;
+    part.logits = static_cast<const T*>(a.logits) + done_rows * a.stride;
+    part.dlogits = static_cast<T*>(a.dlogits) + done_rows * a.dstride;
+    const cudaError_t e =
+        launch_pdl(logprobs_backward_kernel<T>, dim3(static_cast<unsigned>(part.rows * tiles)), dim3(kBackThreads), 0, s,
+                   part, lse + done_rows, dlogprobs + done_rows, static_cast<int32_t>(tiles));
+    if (e != cudaSuccess) return done(e);
+  }
+  return THD_OK;
 }
 
 }  // namespace
@@ -824,12 +896,9 @@ thd_status_t launch_row_loss(RowMode mode, int32_t dtype, const RowArgs& a, cuda
 thd_status_t launch_logprobs_backward(int32_t dtype, const RowArgs& a, const float* lse, const float* dlogprobs,
                                       cudaStream_t s) {
   if (a.rows == 0) return THD_OK;
-  const dim3 grid(static_cast<unsigned>(a.rows)), block(kPlainThreads);
-  if (dtype == THD_DTYPE_BF16)
-    return done(launch_pdl(logprobs_backward_kernel<__nv_bfloat16>, grid, block, 0, s, a, lse, dlogprobs));
-  if (dtype == THD_DTYPE_F16)
-    return done(launch_pdl(logprobs_backward_kernel<__half>, grid, block, 0, s, a, lse, dlogprobs));
-  return done(launch_pdl(logprobs_backward_kernel<float>, grid, block, 0, s, a, lse, dlogprobs));
+  if (dtype == THD_DTYPE_BF16) return launch_backward<__nv_bfloat16>(a, lse, dlogprobs, s);
+  if (dtype == THD_DTYPE_F16) return launch_backward<__half>(a, lse, dlogprobs, s);
+  return launch_backward<float>(a, lse, dlogprobs, s);
 }
 
 }  // namespace thd

@@ -21,7 +21,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib as L
-from .api import ThdError, _need_cuda, _ptr, _raise_host, _range, _stream
+from .api import _NVTX, ThdError, _need_cuda, _raise_host, _range
 
 TOKEN_MEAN = L.TOKEN_MEAN
 DOC_MEAN = L.DOC_MEAN
@@ -60,47 +60,75 @@ def _rows(t, name):
     if t.dim() != 2 or t.shape[1] < 1:
         raise ValueError(f"{name} must be [T, V] with V >= 1, got shape {tuple(t.shape)}")
     T, V = t.shape
-    stride = t.stride(0) if T > 1 else max(t.stride(0), V)
-    if (V > 1 and t.stride(1) != 1) or stride < V:
+    stride, inner = t.stride()
+    if T <= 1 and stride < V:
+        stride = V
+    if (V > 1 and inner != 1) or stride < V:
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {t.stride()}")
     return T, V, stride
 
 
-def _vector(t, name, n, dtype, device):
-    _need_cuda(t, name, dtype)
-    if t.numel() != n:
-        raise ValueError(f"{name} must hold {n} values, got shape {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _vector(t, name, n, dtype, index):
+    """Address of a contiguous vector of n values on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.numel() != n or \
+            t.get_device() != index:
+        _need_cuda(t, name, dtype)  # says what is wrong, or it is one of these:
+        if t.numel() != n:
+            raise ValueError(f"{name} must hold {n} values, got shape {tuple(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     return t.data_ptr()
 
 
-def _optional(t, name, n, dtype, device):
-    return None if t is None else _vector(t, name, n, dtype, device)
+def _optional(t, name, n, dtype, index):
+    return None if t is None else _vector(t, name, n, dtype, index)
 
 
 def _logits(logits, temperature):
     T, V, stride = _rows(logits, "logits")
-    return T, V, L.ThdLogits(logits.data_ptr(), T, stride, V, _DTYPES[logits.dtype], float(temperature), 0)
+    return T, logits.get_device(), L.ThdLogits(logits.data_ptr(), T, stride, V, _DTYPES[logits.dtype],
+                                               temperature, 0)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(n, dtype, device, stream):
     """An output on the stream its kernel runs on: memory that another stream
     still uses is not handed out."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(n, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(n, dtype=dtype, device=device)
 
 
 def _gradient(logits, out, grad_scale, stream):
     """(gradient tensor, its struct); out None: a new contiguous one."""
     if out is None:
         out = _empty(logits.shape, logits.dtype, logits.device, stream)
-    _, _, stride = _rows(out, "out")
-    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
-        raise ValueError("out must match logits in shape, dtype and device")
-    return out, L.ThdGradient(out.data_ptr(), stride, float(grad_scale), 0)
+        row_stride = logits.shape[1]
+    else:
+        _, _, row_stride = _rows(out, "out")
+        if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+            raise ValueError("out must match logits in shape, dtype and device")
+    return out, L.ThdGradient(out.data_ptr(), row_stride, grad_scale, 0)
+
+
+def _call(name, index, stream, status, *args):
+    """One C entry on `stream` (None: the current one of device `index`)."""
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    fn = getattr(L.load(), name)
+    st = None if status is None else _vector(status, "status", 1, torch.int32, index)
+    if _NVTX:
+        with _range(name):
+            code = fn(*args, st, s)
+    else:
+        code = fn(*args, st, s)
+    if code != L.OK:
+        _raise_host(code, name)
+
+
+def _documents(cu_seqlens_padded):
+    n = cu_seqlens_padded.numel() - 1 if isinstance(cu_seqlens_padded, torch.Tensor) else 0
+    if n < 0:
+        raise ThdError(L.ERR_INVALID_ARG, "cu_seqlens_padded holds no boundary")
+    return n
 
 
 def loss_weights(loss_mask, cu_seqlens_padded, cp: int = 1, reduction: int = TOKEN_MEAN, status=None, stream=None):
@@ -111,16 +139,14 @@ def loss_weights(loss_mask, cu_seqlens_padded, cp: int = 1, reduction: int = TOK
     of ``cp`` ranks, or in the contiguous layout (cp = 1).  A row's weight may
     be changed before it is handed to a loss (a normaliser over several
     microbatches, say); a weight of 0 leaves the row out."""
-    _need_cuda(cu_seqlens_padded, "cu_seqlens_padded", torch.int32)
     _need_cuda(loss_mask, "loss_mask", torch.uint8)
-    dev, T, n = loss_mask.device, loss_mask.numel(), cu_seqlens_padded.numel() - 1
-    buf = _empty(2 * T + max(n, 0), torch.int32, dev, stream)
-    weights, doc_ids, ws = buf[:T].view(torch.float32), buf[T:2 * T], buf[2 * T:]
-    with _range("thd_loss_weights"):
-        code = L.load().thd_loss_weights(loss_mask.data_ptr(), cu_seqlens_padded.data_ptr(), n, T, int(cp),
-                                         int(reduction), weights.data_ptr(), doc_ids.data_ptr(), ws.data_ptr(),
-                                         4 * max(n, 0), _ptr(status), _stream(stream))
-    _raise_host(code, "thd_loss_weights")
+    T, dev, n = loss_mask.numel(), loss_mask.get_device(), _documents(cu_seqlens_padded)
+    cu_p = _vector(cu_seqlens_padded, "cu_seqlens_padded", n + 1, torch.int32, dev)
+    weights = _empty(T, torch.float32, loss_mask.device, stream)
+    doc_ids = _empty(T, torch.int32, loss_mask.device, stream)
+    ws = _empty(n, torch.int32, loss_mask.device, stream)
+    _call("thd_loss_weights", dev, stream, status, loss_mask.data_ptr(), cu_p, n, T, cp, reduction,
+          weights.data_ptr(), doc_ids.data_ptr(), ws.data_ptr(), 4 * n)
     return weights, doc_ids
 
 
@@ -128,33 +154,26 @@ def token_logprobs(logits, labels, loss_mask=None, temperature: float = 1.0, sta
     """(logprobs, lse), float32 [T]: the labels' log-probabilities under
     softmax(logits / temperature) and the rows' log-sum-exp.  Rows whose
     loss_mask is 0 are not read and give 0."""
-    T, V, z = _logits(logits, temperature)
-    dev = logits.device
+    T, dev, z = _logits(logits, temperature)
     labels_p = _vector(labels, "labels", T, torch.int32, dev)
     mask_p = _optional(loss_mask, "loss_mask", T, torch.uint8, dev)
-    out = _empty((2, T), torch.float32, dev, stream)
-    p = out.data_ptr()
-    with _range("thd_token_logprobs"):
-        code = L.load().thd_token_logprobs(ctypes.byref(z), labels_p, mask_p, p, p + 4 * T, _ptr(status),
-                                           _stream(stream))
-    _raise_host(code, "thd_token_logprobs")
-    return out[0], out[1]
+    logprobs = _empty(T, torch.float32, logits.device, stream)
+    lse = _empty(T, torch.float32, logits.device, stream)
+    _call("thd_token_logprobs", dev, stream, status, ctypes.byref(z), labels_p, mask_p, logprobs.data_ptr(),
+          lse.data_ptr())
+    return logprobs, lse
 
 
 def token_logprobs_backward(logits, labels, lse, dlogprobs, temperature: float = 1.0, grad_scale: float = 1.0,
                             out=None, status=None, stream=None):
     """dlogits [T, V] of ``token_logprobs`` for the incoming gradient dlogprobs
     [T], rounded once to the logits' type.  ``out`` may be the logits."""
-    T, V, z = _logits(logits, temperature)
-    dev = logits.device
+    T, dev, z = _logits(logits, temperature)
     labels_p = _vector(labels, "labels", T, torch.int32, dev)
     lse_p = _vector(lse, "lse", T, torch.float32, dev)
     g_p = _vector(dlogprobs, "dlogprobs", T, torch.float32, dev)
     out, g = _gradient(logits, out, grad_scale, stream)
-    with _range("thd_token_logprobs_backward"):
-        code = L.load().thd_token_logprobs_backward(ctypes.byref(z), labels_p, lse_p, g_p, ctypes.byref(g),
-                                                    _ptr(status), _stream(stream))
-    _raise_host(code, "thd_token_logprobs_backward")
+    _call("thd_token_logprobs_backward", dev, stream, status, ctypes.byref(z), labels_p, lse_p, g_p, ctypes.byref(g))
     return out
 
 
@@ -166,27 +185,25 @@ def policy_loss(logits, labels, weights, old_logprobs, advantages, ref_logprobs=
 
     advantages: one per row, or with ``doc_ids`` (from loss_weights) one per
     document.  The loss is the weighted sum of the rows' losses."""
-    T, V, z = _logits(logits, temperature)
-    dev = logits.device
+    T, dev, z = _logits(logits, temperature)
     labels_p = _vector(labels, "labels", T, torch.int32, dev)
     weights_p = _vector(weights, "weights", T, torch.float32, dev)
     old_p = _vector(old_logprobs, "old_logprobs", T, torch.float32, dev)
     ref_p = _optional(ref_logprobs, "ref_logprobs", T, torch.float32, dev)
     docs_p = _optional(doc_ids, "doc_ids", T, torch.int32, dev)
-    n_adv = advantages.numel() if docs_p is not None and isinstance(advantages, torch.Tensor) else T
-    adv_p = _vector(advantages, "advantages", n_adv, torch.float32, dev)
+    n_docs = advantages.numel() if docs_p is not None and isinstance(advantages, torch.Tensor) else 0
+    adv_p = _vector(advantages, "advantages", T if docs_p is None else n_docs, torch.float32, dev)
+    g = None
     if need_dlogits:
         out, g = _gradient(logits, out, grad_scale, stream)
-    buf = _empty(3 + 4 * T, torch.float32, dev, stream)
-    base = buf.data_ptr()
-    params = L.ThdPolicy(old_p, ref_p, adv_p, docs_p, n_adv if docs_p is not None else 0, float(clip_low),
-                         float(clip_high), float(kl_coef))
-    with _range("thd_policy_loss"):
-        code = L.load().thd_policy_loss(ctypes.byref(z), labels_p, weights_p, ctypes.byref(params),
-                                        ctypes.byref(g) if need_dlogits else None, base + 12, base, base + 12 + 4 * T,
-                                        12 * T, _ptr(status), _stream(stream))
-    _raise_host(code, "thd_policy_loss")
-    return PolicyLoss(buf[0], buf[1], buf[2], buf[3:3 + T], out if need_dlogits else None)
+    sums = _empty(3, torch.float32, logits.device, stream)
+    logprobs = _empty(T, torch.float32, logits.device, stream)
+    ws = _empty(3 * T, torch.float32, logits.device, stream)
+    params = L.ThdPolicy(old_p, ref_p, adv_p, docs_p, n_docs, clip_low, clip_high, kl_coef)
+    _call("thd_policy_loss", dev, stream, status, ctypes.byref(z), labels_p, weights_p, ctypes.byref(params),
+          None if g is None else ctypes.byref(g), logprobs.data_ptr(), sums.data_ptr(), ws.data_ptr(), 12 * T)
+    loss, kl, clip_fraction = sums.unbind()
+    return PolicyLoss(loss, kl, clip_fraction, logprobs, None if g is None else out)
 
 
 def preference_loss(logprobs, loss_mask, cu_seqlens_padded, chosen, rejected, ref_logprobs=None, cp: int = 1,
@@ -199,25 +216,23 @@ def preference_loss(logprobs, loss_mask, cu_seqlens_padded, chosen, rejected, re
     chosen, rejected: int32 document indices, one pair per entry.  Rows are in
     the zigzag layout of ``cp`` ranks, or contiguous (cp = 1)."""
     _need_cuda(logprobs, "logprobs", torch.float32)
-    _need_cuda(cu_seqlens_padded, "cu_seqlens_padded", torch.int32)
-    dev, T, n = logprobs.device, logprobs.numel(), cu_seqlens_padded.numel() - 1
+    T, dev, n = logprobs.numel(), logprobs.get_device(), _documents(cu_seqlens_padded)
     mask_p = _vector(loss_mask, "loss_mask", T, torch.uint8, dev)
+    cu_p = _vector(cu_seqlens_padded, "cu_seqlens_padded", n + 1, torch.int32, dev)
     ref_p = _optional(ref_logprobs, "ref_logprobs", T, torch.float32, dev)
-    _need_cuda(chosen, "chosen", torch.int32)
-    P = chosen.numel()
+    P = chosen.numel() if isinstance(chosen, torch.Tensor) else 0
+    chosen_p = _vector(chosen, "chosen", P, torch.int32, dev)
     rejected_p = _vector(rejected, "rejected", P, torch.int32, dev)
-    if n < 0:
-        raise ThdError(L.ERR_INVALID_ARG, "preference_loss: cu_seqlens_padded is empty")
-    buf = _empty(1 + P + 3 * n + T, torch.float32, dev, stream)
-    base = buf.data_ptr()
-    params = L.ThdPreference(ref_p, float(beta), float(label_smoothing), float(margin), int(bool(length_normalized)))
-    with _range("thd_preference_loss"):
-        code = L.load().thd_preference_loss(logprobs.data_ptr(), mask_p, cu_seqlens_padded.data_ptr(), n, T, int(cp),
-                                            chosen.data_ptr(), rejected_p, P, ctypes.byref(params), base, base + 4,
-                                            base + 4 * (1 + P), base + 4 * (1 + P + n), base + 4 * (1 + P + n + T),
-                                            8 * n, _ptr(status), _stream(stream))
-    _raise_host(code, "thd_preference_loss")
-    return PreferenceLoss(buf[0], buf[1:1 + P], buf[1 + P:1 + P + n], buf[1 + P + n:1 + P + n + T])
+    loss = _empty((), torch.float32, logprobs.device, stream)
+    margins = _empty(P, torch.float32, logprobs.device, stream)
+    doc_logprobs = _empty(n, torch.float32, logprobs.device, stream)
+    dlogprobs = _empty(T, torch.float32, logprobs.device, stream)
+    ws = _empty(2 * n, torch.float32, logprobs.device, stream)
+    params = L.ThdPreference(ref_p, beta, label_smoothing, margin, length_normalized)
+    _call("thd_preference_loss", dev, stream, status, logprobs.data_ptr(), mask_p, cu_p, n, T, cp, chosen_p,
+          rejected_p, P, ctypes.byref(params), loss.data_ptr(), margins.data_ptr(), doc_logprobs.data_ptr(),
+          dlogprobs.data_ptr(), ws.data_ptr(), 8 * n)
+    return PreferenceLoss(loss, margins, doc_logprobs, dlogprobs)
 
 
 def distill_topk_loss(logits, teacher_ids, teacher_scores, weights, temperature: float = 1.0, normalize: bool = True,
@@ -230,8 +245,7 @@ def distill_topk_loss(logits, teacher_ids, teacher_scores, weights, temperature:
     teacher's logits, over which q = softmax(scores / temperature), or with
     normalize=False its log-probabilities.  The loss is the weighted sum of the
     rows' tau^2 sum_k q_k (ln q_k - lp(id_k))."""
-    T, V, z = _logits(logits, temperature)
-    dev = logits.device
+    T, dev, z = _logits(logits, temperature)
     _need_cuda(teacher_ids, "teacher_ids", torch.int32)
     _need_cuda(teacher_scores, "teacher_scores")
     if teacher_ids.dim() != 2 or teacher_ids.shape[0] != T or teacher_scores.shape != teacher_ids.shape:
@@ -239,18 +253,16 @@ def distill_topk_loss(logits, teacher_ids, teacher_scores, weights, temperature:
                          f"{tuple(teacher_ids.shape)} and {tuple(teacher_scores.shape)}")
     if teacher_scores.dtype not in _DTYPES:
         raise TypeError(f"teacher_scores must be float32, bfloat16 or float16, got {teacher_scores.dtype}")
-    if teacher_ids.device != dev or teacher_scores.device != dev:
-        raise ValueError(f"the teacher's entries must be on {dev}")
+    if teacher_ids.get_device() != dev or teacher_scores.get_device() != dev:
+        raise ValueError(f"the teacher's entries must be on {logits.device}")
     weights_p = _vector(weights, "weights", T, torch.float32, dev)
+    g = None
     if need_dlogits:
         out, g = _gradient(logits, out, grad_scale, stream)
-    buf = _empty(1 + T, torch.float32, dev, stream)
-    base = buf.data_ptr()
+    loss = _empty((), torch.float32, logits.device, stream)
+    token_losses = _empty(T, torch.float32, logits.device, stream)
     teacher = L.ThdTeacher(teacher_ids.data_ptr(), teacher_scores.data_ptr(), teacher_ids.shape[1],
-                           _DTYPES[teacher_scores.dtype], int(bool(normalize)), 0)
-    with _range("thd_distill_topk_loss"):
-        code = L.load().thd_distill_topk_loss(ctypes.byref(z), ctypes.byref(teacher), weights_p,
-                                              ctypes.byref(g) if need_dlogits else None, base + 4, base,
-                                              _ptr(status), _stream(stream))
-    _raise_host(code, "thd_distill_topk_loss")
-    return DistillLoss(buf[0], buf[1:], out if need_dlogits else None)
+                           _DTYPES[teacher_scores.dtype], normalize, 0)
+    _call("thd_distill_topk_loss", dev, stream, status, ctypes.byref(z), ctypes.byref(teacher), weights_p,
+          None if g is None else ctypes.byref(g), token_losses.data_ptr(), loss.data_ptr())
+    return DistillLoss(loss, token_losses, None if g is None else out)
