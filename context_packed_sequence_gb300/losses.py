@@ -27,6 +27,9 @@ TOKEN_MEAN = L.TOKEN_MEAN
 DOC_MEAN = L.DOC_MEAN
 TOKEN_SUM = L.TOKEN_SUM
 
+# the current stream's handle without a torch.cuda.Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 _DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16, torch.float16: L.DTYPE_F16}
 
 
@@ -52,14 +55,15 @@ class DistillLoss(NamedTuple):
 
 
 def _rows(t, name):
-    """A [T, V] CUDA matrix whose rows are dense; returns (T, V, row stride)."""
+    """(T, V, row stride) of a [T, V] CUDA matrix whose rows are dense."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [T, V] with V >= 1, got shape {tuple(t.shape)}")
-    T, V = t.shape
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be [T, V] with V >= 1, got shape {tuple(shape)}")
+    T, V = shape
     stride, inner = t.stride()
     if T <= 1 and stride < V:
         stride = V
@@ -70,56 +74,51 @@ def _rows(t, name):
 
 def _vector(t, name, n, dtype, index):
     """Address of a contiguous vector of n values on CUDA device `index`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.numel() != n or \
-            t.get_device() != index:
-        _need_cuda(t, name, dtype)  # says what is wrong, or it is one of these:
-        if t.numel() != n:
-            raise ValueError(f"{name} must hold {n} values, got shape {tuple(t.shape)}")
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.is_contiguous() and \
+            t.get_device() == index:
+        return t.data_ptr()
+    _need_cuda(t, name, dtype)  # says what is wrong, or it is one of these:
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got shape {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
 def _optional(t, name, n, dtype, index):
     return None if t is None else _vector(t, name, n, dtype, index)
 
 
-def _logits(logits, temperature):
-    T, V, stride = _rows(logits, "logits")
-    return T, logits.get_device(), L.ThdLogits(logits.data_ptr(), T, stride, V, _DTYPES[logits.dtype],
-                                               temperature, 0)
-
-
-def _empty(n, dtype, device, stream):
+def _empty(shape, dtype, device, stream):
     """An output on the stream its kernel runs on: memory that another stream
     still uses is not handed out."""
     if stream is None:
-        return torch.empty(n, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _gradient(logits, out, grad_scale, stream):
+def _gradient(logits, T, V, out, grad_scale, stream):
     """(gradient tensor, its struct); out None: a new contiguous one."""
     if out is None:
-        out = _empty(logits.shape, logits.dtype, logits.device, stream)
-        row_stride = logits.shape[1]
-    else:
-        _, _, row_stride = _rows(out, "out")
-        if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
-            raise ValueError("out must match logits in shape, dtype and device")
+        if stream is None and logits.is_contiguous():
+            out = torch.empty_like(logits)
+        else:
+            out = _empty((T, V), logits.dtype, logits.device, stream)
+        return out, L.ThdGradient(out.data_ptr(), V, grad_scale, 0)
+    _, _, row_stride = _rows(out, "out")
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out must match logits in shape, dtype and device")
     return out, L.ThdGradient(out.data_ptr(), row_stride, grad_scale, 0)
 
 
 def _call(name, index, stream, status, *args):
     """One C entry on `stream` (None: the current one of device `index`)."""
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    fn = getattr(L.load(), name)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
     st = None if status is None else _vector(status, "status", 1, torch.int32, index)
     if _NVTX:
         with _range(name):
-            code = fn(*args, st, s)
+            code = getattr(L.load(), name)(*args, st, s)
     else:
-        code = fn(*args, st, s)
+        code = getattr(L.load(), name)(*args, st, s)
     if code != L.OK:
         _raise_host(code, name)
 
@@ -154,7 +153,9 @@ def token_logprobs(logits, labels, loss_mask=None, temperature: float = 1.0, sta
     """(logprobs, lse), float32 [T]: the labels' log-probabilities under
     softmax(logits / temperature) and the rows' log-sum-exp.  Rows whose
     loss_mask is 0 are not read and give 0."""
-    T, dev, z = _logits(logits, temperature)
+    T, V, row_stride = _rows(logits, "logits")
+    dev = logits.get_device()
+    z = L.ThdLogits(logits.data_ptr(), T, row_stride, V, _DTYPES[logits.dtype], temperature, 0)
     labels_p = _vector(labels, "labels", T, torch.int32, dev)
     mask_p = _optional(loss_mask, "loss_mask", T, torch.uint8, dev)
     logprobs = _empty(T, torch.float32, logits.device, stream)
@@ -168,11 +169,13 @@ def token_logprobs_backward(logits, labels, lse, dlogprobs, temperature: float =
                             out=None, status=None, stream=None):
     """dlogits [T, V] of ``token_logprobs`` for the incoming gradient dlogprobs
     [T], rounded once to the logits' type.  ``out`` may be the logits."""
-    T, dev, z = _logits(logits, temperature)
+    T, V, row_stride = _rows(logits, "logits")
+    dev = logits.get_device()
+    z = L.ThdLogits(logits.data_ptr(), T, row_stride, V, _DTYPES[logits.dtype], temperature, 0)
     labels_p = _vector(labels, "labels", T, torch.int32, dev)
     lse_p = _vector(lse, "lse", T, torch.float32, dev)
     g_p = _vector(dlogprobs, "dlogprobs", T, torch.float32, dev)
-    out, g = _gradient(logits, out, grad_scale, stream)
+    out, g = _gradient(logits, T, V, out, grad_scale, stream)
     _call("thd_token_logprobs_backward", dev, stream, status, ctypes.byref(z), labels_p, lse_p, g_p, ctypes.byref(g))
     return out
 
@@ -185,7 +188,9 @@ def policy_loss(logits, labels, weights, old_logprobs, advantages, ref_logprobs=
 
     advantages: one per row, or with ``doc_ids`` (from loss_weights) one per
     document.  The loss is the weighted sum of the rows' losses."""
-    T, dev, z = _logits(logits, temperature)
+    T, V, row_stride = _rows(logits, "logits")
+    dev = logits.get_device()
+    z = L.ThdLogits(logits.data_ptr(), T, row_stride, V, _DTYPES[logits.dtype], temperature, 0)
     labels_p = _vector(labels, "labels", T, torch.int32, dev)
     weights_p = _vector(weights, "weights", T, torch.float32, dev)
     old_p = _vector(old_logprobs, "old_logprobs", T, torch.float32, dev)
@@ -195,15 +200,16 @@ def policy_loss(logits, labels, weights, old_logprobs, advantages, ref_logprobs=
     adv_p = _vector(advantages, "advantages", T if docs_p is None else n_docs, torch.float32, dev)
     g = None
     if need_dlogits:
-        out, g = _gradient(logits, out, grad_scale, stream)
-    sums = _empty(3, torch.float32, logits.device, stream)
-    logprobs = _empty(T, torch.float32, logits.device, stream)
-    ws = _empty(3 * T, torch.float32, logits.device, stream)
+        out, g = _gradient(logits, T, V, out, grad_scale, stream)
+    # logprobs [T], the loss, its KL term and the clipped share, then the call's workspace [3 T]
+    buf = _empty(4 * T + 3, torch.float32, logits.device, stream)
+    base = buf.data_ptr()
     params = L.ThdPolicy(old_p, ref_p, adv_p, docs_p, n_docs, clip_low, clip_high, kl_coef)
     _call("thd_policy_loss", dev, stream, status, ctypes.byref(z), labels_p, weights_p, ctypes.byref(params),
-          None if g is None else ctypes.byref(g), logprobs.data_ptr(), sums.data_ptr(), ws.data_ptr(), 12 * T)
-    loss, kl, clip_fraction = sums.unbind()
-    return PolicyLoss(loss, kl, clip_fraction, logprobs, None if g is None else out)
+          None if g is None else ctypes.byref(g), base, base + 4 * T, base + 4 * T + 12, 12 * T)
+    part = buf.as_strided
+    return PolicyLoss(part((), (), T), part((), (), T + 1), part((), (), T + 2), part((T,), (1,), 0),
+                      None if g is None else out)
 
 
 def preference_loss(logprobs, loss_mask, cu_seqlens_padded, chosen, rejected, ref_logprobs=None, cp: int = 1,
@@ -223,16 +229,15 @@ def preference_loss(logprobs, loss_mask, cu_seqlens_padded, chosen, rejected, re
     P = chosen.numel() if isinstance(chosen, torch.Tensor) else 0
     chosen_p = _vector(chosen, "chosen", P, torch.int32, dev)
     rejected_p = _vector(rejected, "rejected", P, torch.int32, dev)
-    loss = _empty((), torch.float32, logprobs.device, stream)
-    margins = _empty(P, torch.float32, logprobs.device, stream)
-    doc_logprobs = _empty(n, torch.float32, logprobs.device, stream)
-    dlogprobs = _empty(T, torch.float32, logprobs.device, stream)
-    ws = _empty(2 * n, torch.float32, logprobs.device, stream)
+    # dlogprobs [T], margins [P], doc_logprobs [n], the loss, then the call's workspace [2 n]
+    buf = _empty(T + P + 3 * n + 1, torch.float32, logprobs.device, stream)
+    base = buf.data_ptr()
     params = L.ThdPreference(ref_p, beta, label_smoothing, margin, length_normalized)
     _call("thd_preference_loss", dev, stream, status, logprobs.data_ptr(), mask_p, cu_p, n, T, cp, chosen_p,
-          rejected_p, P, ctypes.byref(params), loss.data_ptr(), margins.data_ptr(), doc_logprobs.data_ptr(),
-          dlogprobs.data_ptr(), ws.data_ptr(), 8 * n)
-    return PreferenceLoss(loss, margins, doc_logprobs, dlogprobs)
+          rejected_p, P, ctypes.byref(params), base + 4 * (T + P + n), base + 4 * T, base + 4 * (T + P), base,
+          base + 4 * (T + P + n + 1), 8 * n)
+    part = buf.as_strided
+    return PreferenceLoss(part((), (), T + P + n), part((P,), (1,), T), part((n,), (1,), T + P), part((T,), (1,), 0))
 
 
 def distill_topk_loss(logits, teacher_ids, teacher_scores, weights, temperature: float = 1.0, normalize: bool = True,
@@ -245,7 +250,9 @@ def distill_topk_loss(logits, teacher_ids, teacher_scores, weights, temperature:
     teacher's logits, over which q = softmax(scores / temperature), or with
     normalize=False its log-probabilities.  The loss is the weighted sum of the
     rows' tau^2 sum_k q_k (ln q_k - lp(id_k))."""
-    T, dev, z = _logits(logits, temperature)
+    T, V, row_stride = _rows(logits, "logits")
+    dev = logits.get_device()
+    z = L.ThdLogits(logits.data_ptr(), T, row_stride, V, _DTYPES[logits.dtype], temperature, 0)
     _need_cuda(teacher_ids, "teacher_ids", torch.int32)
     _need_cuda(teacher_scores, "teacher_scores")
     if teacher_ids.dim() != 2 or teacher_ids.shape[0] != T or teacher_scores.shape != teacher_ids.shape:
@@ -258,7 +265,7 @@ def distill_topk_loss(logits, teacher_ids, teacher_scores, weights, temperature:
     weights_p = _vector(weights, "weights", T, torch.float32, dev)
     g = None
     if need_dlogits:
-        out, g = _gradient(logits, out, grad_scale, stream)
+        out, g = _gradient(logits, T, V, out, grad_scale, stream)
     loss = _empty((), torch.float32, logits.device, stream)
     token_losses = _empty(T, torch.float32, logits.device, stream)
     teacher = L.ThdTeacher(teacher_ids.data_ptr(), teacher_scores.data_ptr(), teacher_ids.shape[1],
