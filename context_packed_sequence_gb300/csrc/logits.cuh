@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <cstring>
 
 #include "thd_internal.cuh"
 
@@ -21,6 +22,7 @@ namespace thd {
 struct LogitScale {
   float hi, lo;
   float tau, inv_tau;
+  uint64_t hi2, lo2;  // {hi, hi} and {lo, lo} for the packed instructions
 };
 
 inline LogitScale make_logit_scale(float temperature) {
@@ -31,6 +33,11 @@ inline LogitScale make_logit_scale(float temperature) {
   s.hi = static_cast<float>(c);
   if (static_cast<double>(s.hi) >= c) s.hi = std::nextafterf(s.hi, 0.0f);
   s.lo = static_cast<float>(c - static_cast<double>(s.hi));
+  uint32_t bits;
+  std::memcpy(&bits, &s.hi, 4);
+  s.hi2 = uint64_t(bits) << 32 | bits;
+  std::memcpy(&bits, &s.lo, 4);
+  s.lo2 = uint64_t(bits) << 32 | bits;
   return s;
 }
 
@@ -41,7 +48,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // 2^(d * log2(e) * inv_tau) = exp(d * inv_tau)
-__device__ __forceinline__ float exp_scaled(float d, LogitScale c) { return ex2(fmaf(d, c.hi, d * c.lo)); }
+__device__ __forceinline__ float exp_scaled(float d, const LogitScale& c) { return ex2(fmaf(d, c.hi, d * c.lo)); }
 
 // ---------------------------------------------------------------------------
 // element types
@@ -139,7 +146,7 @@ __device__ __forceinline__ SoftmaxStat empty_stat() { return {-INFINITY, {0.0f, 
 // The sum of a set with maximum m, rescaled to the shift of the larger maximum
 // `to`.  One factor scales a whole partial sum, so the rounding of its
 // exponent and the mean error of ex2 go into the low part.
-__device__ __forceinline__ Pair rescaled(float m, Pair s, float to, LogitScale c) {
+__device__ __forceinline__ Pair rescaled(float m, Pair s, float to, const LogitScale& c) {
   if (m == to || s.hi == 0.0f) return s;
   const float d = softmax_shift(m) - softmax_shift(to);
   const float x = d * c.hi;
@@ -170,11 +177,11 @@ __device__ __forceinline__ RowNorm row_norm(SoftmaxStat t) {
 
 // Logarithm of the probability of a logit z, as a pair.  Its error is that of
 // the sum: the large numbers z and m are subtracted before anything is rounded.
-__device__ __forceinline__ Pair log_prob(float z, const RowNorm& r, LogitScale c) {
+__device__ __forceinline__ Pair log_prob(float z, const RowNorm& r, const LogitScale& c) {
   return add(scaled(two_sum(z, -r.shift), c.inv_tau, 0.0f), {-r.log_sum.hi, -r.log_sum.lo});
 }
 
-__device__ __forceinline__ float log_sum_exp(const RowNorm& r, LogitScale c) {
+__device__ __forceinline__ float log_sum_exp(const RowNorm& r, const LogitScale& c) {
   const Pair n = add(scaled({r.shift, 0.0f}, c.inv_tau, 0.0f), r.log_sum);
   return n.hi + n.lo;
 }

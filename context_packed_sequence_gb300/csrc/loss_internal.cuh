@@ -52,9 +52,11 @@ struct RowGrad {
 // statistics are known.
 struct RowHead {
   float weight;   // 0: the row takes no part
+  float mass;     // ROW_DISTILL: sum of the teacher's probabilities
   float z_label;
   float old_lp, ref_lp, advantage;
   int32_t label;
+  int32_t fetched;  // the row had weight (and its label may be bad)
 };
 
 template <typename T, int kMode>
@@ -63,6 +65,7 @@ __device__ __forceinline__ RowHead row_head(const RowArgs& a, int64_t t) {
   h.label = -1;
   if (kMode == ROW_SCORE) h.weight = (!a.mask || a.mask[t]) ? 1.0f : 0.0f;
   else h.weight = a.weights[t];
+  h.fetched = h.weight != 0.0f;
   if (h.weight == 0.0f || kMode == ROW_DISTILL) return h;
   h.label = a.labels[t];
   bool ok = h.label >= 0 && h.label < a.vocab;
@@ -98,7 +101,7 @@ __device__ __forceinline__ void write_idle_row(const RowArgs& a, int64_t t) {
 
 // Log-probability of the label; a row without any logit above -inf gives it
 // -inf (the quotient 0 / 0 of the formula has no value).
-__device__ __forceinline__ Pair label_logprob(float z, SoftmaxStat st, const RowNorm& r, LogitScale c) {
+__device__ __forceinline__ Pair label_logprob(float z, SoftmaxStat st, const RowNorm& r, const LogitScale& c) {
   if (stat_is_empty(st) && z == -INFINITY) return {-INFINITY, 0.0f};
   return log_prob(z, r, c);
 }
@@ -243,7 +246,7 @@ __device__ __forceinline__ float entry_mass(const Teacher& s, int32_t id, int32_
 
 // The student's log-probability of an entry; `empty`: no logit of the row is
 // above -inf
-__device__ __forceinline__ Pair entry_logprob(float z, bool empty, const RowNorm& r, LogitScale c) {
+__device__ __forceinline__ Pair entry_logprob(float z, bool empty, const RowNorm& r, const LogitScale& c) {
   return empty ? Pair{-INFINITY, 0.0f} : log_prob(z, r, c);
 }
 

@@ -161,48 +161,47 @@ struct Word<float> {
   }
 };
 
-// Maximum of kVecs vectors, in the elements' type: NaNs are passed over (the
-// sum of exponentials shows them).
-template <typename T, int kVecs>
-__device__ __forceinline__ float vector_max(const uint4 (&v)[kVecs]) {
-  uint32_t m = Word<T>::kNegInf;
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u)
-    m = Word<T>::max2(Word<T>::max2(Word<T>::max2(m, v[u].x), Word<T>::max2(v[u].y, v[u].z)), v[u].w);
-  return Word<T>::top(m);
+// Maximum of a packed running maximum and a vector, in the elements' type:
+// NaNs are passed over (the sum of exponentials shows them).
+template <typename T>
+__device__ __forceinline__ uint32_t max_vector(uint32_t m, const uint4& v) {
+  return Word<T>::max2(Word<T>::max2(Word<T>::max2(m, v.x), Word<T>::max2(v.y, v.z)), v.w);
 }
 
-// A thread's running softmax statistics over batches of logits: the maximum
-// of a batch first, so that a rescaling costs one branch a batch.
-struct ThreadStat {
-  float m = -INFINITY;
-  Pair s = {0.0f, 0.0f};
+// Sums of exp((z - shift) * inv_tau) over vectors.
+struct ExpSum {
+  uint64_t neg, acc[2];
 
-  __device__ __forceinline__ void raise(float to, LogitScale c) {
-    if (to > m) {
-      s = rescaled(m, s, to, c);
-      m = to;
+  __device__ __forceinline__ explicit ExpSum(float shift) : neg(pack2(-shift, -shift)), acc{0, 0} {}
+  template <typename T>
+  __device__ __forceinline__ void add(const uint4& v, const LogitScale& c) {
+#pragma unroll
+    for (int i = 0; i < Word<T>::kPairs; ++i) {
+      const uint64_t d = add2(Word<T>::pair(v, i), neg);
+      acc[i & 1] = add2(acc[i & 1], ex2_2(fma2(d, c.hi2, mul2(d, c.lo2))));
     }
   }
-  __device__ __forceinline__ void add_one(float z, LogitScale c) {
-    raise(z, c);
-    s.hi += exp_scaled(z - softmax_shift(m), c);
-  }
-  template <typename T, int kVecs>
-  __device__ __forceinline__ void add_vectors(const uint4 (&v)[kVecs], LogitScale c) {
-    raise(vector_max<T, kVecs>(v), c);
-    const float shift = softmax_shift(m);
-    const uint64_t neg = pack2(-shift, -shift), hi = pack2(c.hi, c.hi), lo = pack2(c.lo, c.lo);
-    uint64_t acc[2] = {0, 0};
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u)
-#pragma unroll
-      for (int i = 0; i < Word<T>::kPairs; ++i) {
-        const uint64_t d = add2(Word<T>::pair(v[u], i), neg);
-        acc[i & 1] = add2(acc[i & 1], ex2_2(fma2(d, hi, mul2(d, lo))));
-      }
+  __device__ __forceinline__ float total() const {
     const float2 t = unpack2(add2(acc[0], acc[1]));
-    s.hi += t.x + t.y;
+    return t.x + t.y;
+  }
+};
+
+// k * exp((z - shift) * inv_tau) of a vector, rounded to its type.
+struct Gradient {
+  uint64_t neg, k2;
+
+  __device__ __forceinline__ Gradient(float shift, float k) : neg(pack2(-shift, -shift)), k2(pack2(k, k)) {}
+  template <typename T>
+  __device__ __forceinline__ uint4 of(const uint4& v, const LogitScale& c) const {
+    uint4 d;
+#pragma unroll
+    for (int j = 0; j < Word<T>::kPairs; ++j)
+      Word<T>::set_pair(d, j, mul2(k2, ex2_2(mul2(add2(Word<T>::pair(v, j), neg), c.hi2))));
+    return d;
+  }
+  __device__ __forceinline__ float of(float z, const LogitScale& c) const {
+    return unpack2(k2).x * ex2((z + unpack2(neg).x) * c.hi);
   }
 };
 
@@ -212,38 +211,18 @@ __device__ __forceinline__ float warp_max_one(float v) {
   return r;
 }
 
-// The block's statistics, in every thread of its first warp.  `failed` comes
-// back true in every thread when it was in any.
-__device__ __forceinline__ SoftmaxStat block_stat(ThreadStat t, LogitScale c, float* maxima, Pair* sums, bool* failed) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  float m = warp_max_one(t.m);
-  if (lane == 0) maxima[wid] = m;
-  *failed = __syncthreads_or(*failed);
-  m = maxima[0];
-  for (int w = 1; w < nw; ++w) m = fmaxf(m, maxima[w]);
-  const Pair own = unbiased_sum(t.s.hi);
-  Pair s = rescaled(t.m, {t.s.hi, t.s.lo + own.lo}, m, c);
-  // high and low parts each on their own: a few roundings of 6e-8 at random
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.hi += __shfl_xor_sync(kFullMask, s.hi, o);
-    s.lo += __shfl_xor_sync(kFullMask, s.lo, o);
-  }
-  if (lane == 0) sums[wid] = s;
-  __syncthreads();
-  if (wid == 0) {
-    s = {0.0f, 0.0f};
-    for (int w = 0; w < nw; ++w) s = add(s, sums[w]);
-  }
-  return {m, s};
+// Barrier of the first kThreads threads of a block.
+template <int kThreads>
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
 // A row's gradient as its threads need it, from the first warp to the block.
 struct RowResult {
   SoftmaxStat st;
   RowGrad g;
-  float mass;
-  bool failed;
+  bool stop;  // something failed: nothing more is written
+  bool idle;  // the row takes no part after all
 };
 
 // kThreads threads; every entry of the teacher is some thread's.
@@ -256,10 +235,11 @@ struct EntryFix {
 // Loss terms of the entries for which `mine(id)` and their gradients;
 // `logit(id)` reads the row.  Returns this thread's part of the loss / tau^2.
 template <int kThreads, class Mine, class Logit>
-__device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher& te, float weight, const RowResult& r,
-                                                 Mine mine, Logit logit, EntryFix<kThreads>& fix) {
+__device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher& te, const RowHead& h,
+                                                 const RowResult& r, Mine mine, Logit logit,
+                                                 EntryFix<kThreads>& fix) {
   const RowNorm norm = row_norm(r.st);
-  const float gs = a.grad_scale * weight * a.scale.tau;
+  const float gs = a.grad_scale * h.weight * a.scale.tau;
   const bool empty = stat_is_empty(r.st);
   float loss = 0.0f;
 #pragma unroll
@@ -271,7 +251,7 @@ __device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher
     if (id < 0 || !mine(id)) continue;
     const Pair lp = entry_logprob(logit(id), empty, norm, a.scale);
     if (te.q[k] != 0.0f) loss += te.q[k] * ((te.lq[k] - lp.hi) - lp.lo);
-    fix.at[j] = empty ? 0.0f : gs * (r.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
+    fix.at[j] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
   }
   return loss;
 }
@@ -288,14 +268,29 @@ __device__ __forceinline__ void write_entries(const RowArgs& a, const Teacher& t
   }
 }
 
-__device__ __forceinline__ float block_sum(float v, float* tmp) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+template <int kThreads>
+__device__ __forceinline__ float group_sum(float v, float* tmp) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   v = warp_sum(v);
   if (lane == 0) tmp[wid] = v;
-  __syncthreads();
+  group_sync<kThreads>();
   v = 0.0f;
-  for (int w = 0; w < nw; ++w) v += tmp[w];
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += tmp[w];
   return v;
+}
+
+// The scalars of a row and the coefficients of its gradient, from its
+// statistics; by a whole warp, `write`: this block reports them.
+template <int kMode>
+__device__ __forceinline__ RowGrad finish_row(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st,
+                                              bool write) {
+  if (kMode == ROW_SCORE) {
+    if (write) write_score(a, t, h, st);
+    return {0.0f, 0.0f};
+  }
+  if (kMode == ROW_POLICY) return policy_row(a, t, h, st, write);
+  return {stat_is_empty(st) ? 0.0f : a.grad_scale * h.weight * a.scale.tau * h.mass / st.s.hi, 0.0f};
 }
 
 // ---------------------------------------------------------------------------
@@ -303,7 +298,8 @@ __device__ __forceinline__ float block_sum(float v, float* tmp) {
 // ---------------------------------------------------------------------------
 
 constexpr int kVecsPerStep = 4;  // vectors a thread holds in registers at a time
-constexpr int kMaxChunks = 16;   // parts of a slice that arrive on their own
+constexpr int kChunkSteps = 2;   // steps in a part of a slice that arrives on its own
+constexpr int kMaxChunks = 8;    // chunks of all buffers
 constexpr int kMaxCluster = 8;   // largest portable cluster
 constexpr int kMaxSlice = 208 * 1024;
 
@@ -312,17 +308,58 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Every block of the cluster runs, and its barriers are set up, once each has
-// arrived (after its fence.mbarrier_init) and this one has waited.  By whole
-// warps.
-__device__ __forceinline__ void cluster_arrive() {
+// All threads of the cluster, by whole warps; what they wrote before is
+// visible to the others after.
+__device__ __forceinline__ void cluster_sync() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// The int that block 0 of the cluster has at this block's address of it.
+__device__ __forceinline__ int32_t cluster_load0(const int32_t* at) {
+  uint32_t remote;
+  int32_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_addr(at)));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
 }
+// One arrival on block 0's barrier.
+__device__ __forceinline__ void cluster_arrive0(const uint64_t* bar) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_addr(bar)));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+// Work taken from clusters of this grid that have not started yet (PTX ISA,
+// clusterlaunchcontrol): the request asks for one such cluster, whose first
+// block index, or that none is left, arrives in every block's slot.
+__device__ __forceinline__ void request_row(void* slot, uint64_t* bar, bool to_cluster) {
+  if (to_cluster)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+        "[%0], [%1];" ::"r"(smem_addr(slot)),
+        "r"(smem_addr(bar))
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(slot)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// The first block index of the cluster that was taken, -1 for none.
+__device__ __forceinline__ int32_t requested_block(const void* slot) {
+  uint32_t x, got;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n .reg .b32 y, z;\n ld.shared.b128 h, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %1, 1, 0, p;\n mov.u32 %0, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, h;\n}\n"
+      : "=r"(x), "=r"(got)
+      : "r"(smem_addr(slot))
+      : "memory");
+  fence_proxy_async_shared();  // the slot may be written again
+  return got ? static_cast<int32_t>(x) : -1;
+}
+
 // A float4 into block `rank`'s shared memory, at this block's addresses of the
 // slot and of the barrier that counts its 16 bytes.
 __device__ __forceinline__ void cluster_send(const float4* at, const uint64_t* bar, uint32_t rank, float4 v) {
@@ -335,14 +372,14 @@ __device__ __forceinline__ void cluster_send(const float4* at, const uint64_t* b
       : "memory");
 }
 // Bounded wait for what the cluster sends here (like mbar_wait).
-__device__ __forceinline__ bool cluster_receive(uint64_t* bar) {
+__device__ __forceinline__ bool cluster_receive(uint64_t* bar, uint32_t parity) {
   for (int it = 0; it < kWaitLimit; ++it) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
-        : "r"(smem_addr(bar))
+        : "r"(smem_addr(bar)), "r"(parity)
         : "memory");
     if (done) return true;
   }
@@ -391,231 +428,449 @@ __device__ __forceinline__ int32_t edge_index(const Slice& s, int32_t i, int32_t
   return i < s.head ? i : V - (s.edge_count - i);
 }
 
-template <typename T, int kMode, int kThreads>
-__global__ void __launch_bounds__(kThreads) row_cluster_kernel(const __grid_constant__ RowArgs a, int32_t cluster_log2) {
+template <typename T, int kThreads>
+__device__ __forceinline__ void zero_slice(T* dz, const Slice& sl, int32_t V) {
   constexpr int N = Word<T>::kElems;
-  constexpr int kStep = kThreads * kVecsPerStep;  // vectors of a chunk
+  T* dv = dz + sl.head + static_cast<int64_t>(sl.first) * N;
+  if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+    uint4* to = reinterpret_cast<uint4*>(dv);
+#pragma unroll 4
+    for (int32_t i = threadIdx.x; i < sl.count; i += kThreads) to[i] = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(sl.count) * N; i += kThreads) dv[i] = from_float<T>(0.0f);
+  }
+  if (static_cast<int32_t>(threadIdx.x) < sl.edge_count) dz[edge_index(sl, threadIdx.x, V)] = from_float<T>(0.0f);
+}
+
+// How a launch lays out its blocks' shared memory.
+struct RingShape {
+  int32_t cluster_log2;
+  int32_t buffers;  // row slices held at a time
+  int32_t chunks;   // chunks of a slice (the last ones may be empty)
+  int32_t vecs;     // vectors a buffer holds
+};
+
+// Bounded wait that gives up at once when the block is told to quit, and tells
+// the rest of the block to when it runs out.
+__device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, volatile int32_t* quit) {
+  for (int it = 0; it < kWaitLimit; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*quit) return false;
+  }
+  *quit = 1;
+  return false;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A row as the block's warps see it.
+struct RowJob {
+  int32_t row;      // -1: no more
+  int32_t fetched;  // it has weight, so its logits are fetched
+  Slice slice;
+};
+
+// The grid has a cluster for every row; those that run take the rows of those
+// that have not started, so a cluster's blocks stay for many rows and yet no
+// cluster is left with more than its share.  kWarps warps compute.  One more
+// fetches the slices into a ring of buffers, chunk by chunk as they become
+// free, and another finds the next row and reads what it needs besides its
+// logits, up to two rows ahead.
+template <typename T, int kMode, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
+    row_cluster_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
+  constexpr int N = Word<T>::kElems;
+  constexpr int kThreads = kWarps * 32;
+  constexpr int kStep = kThreads * kVecsPerStep;  // vectors of a step
+  constexpr int kChunk = kStep * kChunkSteps;     // vectors of a chunk
   constexpr uint32_t kNone = Word<T>::kNegInf;
-  extern __shared__ __align__(128) unsigned char dynamic[];
-  __shared__ uint64_t bars[kMaxChunks];
-  __shared__ uint64_t stat_bar, loss_bar;
-  __shared__ float maxima[kThreads / 32];
-  __shared__ Pair sums[kThreads / 32];
-  __shared__ __align__(16) float4 inbox[kMaxCluster];     // each block's statistics
-  __shared__ __align__(16) float4 loss_box[kMaxCluster];  // each block's part of the distillation loss
-  __shared__ RowHead head;
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ uint64_t full[kMaxChunks], empty[kMaxChunks];    // of each chunk of each buffer
+  __shared__ uint64_t job_full[2], job_empty[2], head_full[2], stat_bar[2], next_full[2], next_free[2];
+  __shared__ uint64_t loss_bar[kMode == ROW_DISTILL ? 2 : 1];
+  __shared__ float maxima[kWarps], parts[2][kWarps];
+  __shared__ __align__(16) float4 next[2];                    // answers to requests for rows
+  __shared__ __align__(16) float4 inbox[2][kMaxCluster];      // each block's statistics of a row
+  // each block's part of a distillation loss
+  __shared__ __align__(16) float4 loss_box[kMode == ROW_DISTILL ? 2 : 1][kMode == ROW_DISTILL ? kMaxCluster : 1];
+  __shared__ RowJob jobs[2];
+  __shared__ RowHead heads[2];
   __shared__ RowResult result;
+  __shared__ volatile int32_t quit;
   __shared__ int32_t stop;
 
-  pdl_wait_then_release();
-  const int tid = threadIdx.x;
-  const int32_t cluster = 1 << cluster_log2;
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int32_t cluster = 1 << shape.cluster_log2;
   const int32_t rank = cluster > 1 ? static_cast<int32_t>(cluster_rank()) : 0;
-  const int64_t t = blockIdx.x >> cluster_log2;
-  const T* z = static_cast<const T*>(a.logits) + t * a.stride;
-  T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
-  const Slice sl = row_slice(z, a.vocab, rank, cluster_log2);
-  uint4* buf = reinterpret_cast<uint4*>(dynamic);
-  const int32_t chunks = (sl.count + kStep - 1) / kStep;
-
-  bool loading = false;
   if (tid == 0) {
-    const int32_t s = status_load(a.status);
-    float w;
-    if (kMode == ROW_SCORE) w = (!a.mask || a.mask[t]) ? 1.0f : 0.0f;
-    else w = a.weights[t];
-    stop = s;
-    loading = s == 0 && w != 0.0f;
-    for (int i = 0; i < chunks; ++i) mbar_init(&bars[i], 1);
-    if (cluster > 1) {
-      mbar_init(&stat_bar, 1);
-      mbar_init(&loss_bar, 1);
+    quit = 0;
+    for (int i = 0; i < shape.buffers * shape.chunks; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&job_full[i], 1);
+      mbar_init(&job_empty[i], kWarps + 1);
+      mbar_init(&head_full[i], 1);
+      mbar_init(&stat_bar[i], 1);
+      mbar_init(&next_full[i], 1);
+      mbar_init(&next_free[i], cluster);
+      if (cluster > 1) mbar_arrive_expect_tx(&stat_bar[i], 16 * cluster);
+      if (kMode == ROW_DISTILL) {
+        mbar_init(&loss_bar[i], 1);
+        if (cluster > 1 && rank == 0) mbar_arrive_expect_tx(&loss_bar[i], 16 * cluster);
+      }
     }
     mbar_init_fence();
-    if (loading) {
-      const uint4* zv = reinterpret_cast<const uint4*>(z + sl.head) + sl.first;
-      for (int i = 0; i < chunks; ++i) {
-        const int32_t n = min(kStep, sl.count - i * kStep) * 16;
-        mbar_arrive_expect_tx(&bars[i], n);
-        bulk_load(buf + i * kStep, zv + i * kStep, n, &bars[i]);
-      }
-    }
-    if (cluster > 1) {
-      mbar_arrive_expect_tx(&stat_bar, 16 * cluster);
-      if (kMode == ROW_DISTILL && rank == 0) mbar_arrive_expect_tx(&loss_bar, 16 * cluster);
-    }
-  } else if (tid == 32) {
-    head = row_head<T, kMode>(a, t);
   }
-  if (cluster > 1) cluster_arrive();
+  pdl_wait_then_release();
+  if (tid == 0 && rank == 0) stop = status_load(a.status);
+  if (cluster > 1) cluster_sync();
+  if (tid == 0 && rank != 0) stop = cluster_load0(&stop);
   __syncthreads();
-  const RowHead h = head;
-  if (cluster > 1) cluster_wait();
-  // Every block of the cluster reads the same weight and label, so all of
-  // them take this branch or none; the status word may change meanwhile, so
-  // a block that saw it set goes on and tells the others.
-  if (h.weight == 0.0f) {
-    if (loading)  // a bad label: the copies have to land before the block ends
-      for (int i = 0; i < chunks; ++i) mbar_wait(&bars[i], 0);
-    if (stop) return;
-    if (tid == 0 && rank == 0) write_idle_row<kMode>(a, t);
-    if (!dz) return;
-    const T zero = from_float<T>(0.0f);
-    T* dv = dz + sl.head + static_cast<int64_t>(sl.first) * N;
-    if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
-#pragma unroll 4
-      for (int32_t i = tid; i < sl.count; i += kThreads) reinterpret_cast<uint4*>(dv)[i] = make_uint4(0, 0, 0, 0);
-    } else {
-      for (int64_t i = tid; i < static_cast<int64_t>(sl.count) * N; i += kThreads) dv[i] = zero;
+
+  uint4* const ring = reinterpret_cast<uint4*>(dynamic);
+  unsigned char* const teachers = dynamic + static_cast<size_t>(shape.buffers) * shape.vecs * 16;
+
+  if (stop) {
+    // the whole cluster does nothing
+  } else if (wid == kWarps) {
+    // ---- the slices
+    if (lane == 0) {
+      int32_t slot = 0, used = 0;  // the chunk to fill; chunks filled at least once
+      uint32_t phase = 0;          // of the ring
+      const int32_t slots = shape.buffers * shape.chunks;
+      bool ok = true;
+      for (int32_t k = 0; ok; ++k) {
+        if (!(ok = wait_or_quit(&job_full[k & 1], (k >> 1) & 1, &quit))) break;
+        const RowJob job = jobs[k & 1];
+        mbar_arrive(&job_empty[k & 1]);
+        if (job.row < 0) break;
+        if (!job.fetched) continue;
+        const T* z = static_cast<const T*>(a.logits) + job.row * a.stride;
+        const uint4* from = reinterpret_cast<const uint4*>(z + job.slice.head) + job.slice.first;
+        uint4* to = ring + slot / shape.chunks * shape.vecs;
+        for (int32_t left = job.slice.count, j = 0; j < shape.chunks; ++j, left -= kChunk, from += kChunk, to += kChunk) {
+          if (!(ok = wait_or_quit(&empty[slot], phase ^ 1u, &quit))) break;
+          const int32_t bytes = min(kChunk, max(0, left)) * 16;
+          mbar_arrive_expect_tx(&full[slot], bytes);
+          if (bytes > 0) bulk_load(to, from, bytes, &full[slot]);
+          used = max(used, ++slot);
+          if (slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy has to land before the block ends, whether its row is still
+      // wanted or not: chunk i was last filled in this pass over the ring if
+      // it lies before `slot`, else in the one before.
+      for (int32_t i = 0; i < used; ++i) mbar_wait(&full[i], i < slot ? phase : phase ^ 1u);
     }
-    if (tid < sl.edge_count) dz[edge_index(sl, tid, a.vocab)] = zero;
-    return;
-  }
-
-  bool failed = stop != 0;
-  const Teacher te = teacher_at(dynamic + static_cast<size_t>(sl.count) * 16, a.teacher_count);
-  float mass = 0.0f;
-  if (kMode == ROW_DISTILL && tid < 32 && !failed) mass = load_teacher(a, t, te, rank == 0);
-
-  // the slice's statistics, chunk by chunk as they land
-  ThreadStat ts;
-  if (!failed) {
-    const uint4* from = buf + tid;
-    for (int i = 0; i < chunks; ++i, from += kStep) {
-      if (!mbar_wait(&bars[i], 0)) {
-        failed = true;
+  } else if (wid == kWarps + 1) {
+    // ---- which rows, their scalars and teacher entries
+    int32_t row = static_cast<int32_t>(blockIdx.x >> shape.cluster_log2);
+    bool ok = true;
+    for (int32_t k = 0; ok; ++k) {
+      float weight = 0.0f;
+      if (row >= 0) {
+        // ask for row k + 1: its slot is free once every block has read row k - 1 from it
+        const int i = (k + 1) & 1;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&next_full[i], 16);
+          if (rank == 0) {
+            ok = wait_or_quit(&next_free[i], ((k >> 1) & 1) ^ 1, &quit);
+            if (ok) request_row(&next[i], &next_full[i], cluster > 1);
+          }
+        }
+        ok = __shfl_sync(kFullMask, ok, 0);
+        if (kMode == ROW_SCORE) weight = (!a.mask || a.mask[row]) ? 1.0f : 0.0f;
+        else weight = a.weights[row];
+      }
+      if (!ok || !(ok = wait_or_quit(&job_empty[k & 1], ((k >> 1) & 1) ^ 1, &quit))) break;
+      if (lane == 0) {
+        RowJob job;
+        job.row = row;
+        job.fetched = weight != 0.0f;
+        job.slice = row_slice(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, shape.cluster_log2);
+        jobs[k & 1] = job;
+        mbar_arrive(&job_full[k & 1]);
+      }
+      if (row < 0) break;
+      if (weight != 0.0f) {
+        RowHead h;
+        if (lane == 0) h = row_head<T, kMode>(a, row);
+        if (kMode == ROW_DISTILL) {
+          const Teacher te = teacher_at(teachers + (k & 1) * teacher_bytes(a.teacher_count), a.teacher_count);
+          h.mass = load_teacher(a, row, te, rank == 0);
+        }
+        if (lane == 0) heads[k & 1] = h;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&head_full[k & 1]);
+      // the answer, which every block of the cluster gets
+      const int i = (k + 1) & 1;
+      if (!(ok = cluster_receive(&next_full[i], (k >> 1) & 1))) {
+        quit = 1;
         break;
       }
-      const int32_t left = sl.count - i * kStep;
-      uint4 v[kVecsPerStep];
-      if (left >= kStep) {
-#pragma unroll
-        for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
-      } else {
-#pragma unroll
-        for (int u = 0; u < kVecsPerStep; ++u)
-          v[u] = u * kThreads + tid < left ? from[u * kThreads] : make_uint4(kNone, kNone, kNone, kNone);
-      }
-      ts.add_vectors<T, kVecsPerStep>(v, a.scale);
+      const int32_t block = requested_block(&next[i]);
+      row = block < 0 ? -1 : block >> shape.cluster_log2;
+      __syncwarp();
+      if (lane == 0) cluster_arrive0(&next_free[i]);
     }
-    if (tid < sl.edge_count) ts.add_one(to_float(z[edge_index(sl, tid, a.vocab)]), a.scale);
-    if (failed) status_set(a.status, THD_ERR_TIMEOUT);
-  }
-  SoftmaxStat st = block_stat(ts, a.scale, maxima, sums, &failed);
-  if (tid < 32) {
-    bool off = failed;
-    if (cluster > 1) {
-      if (tid < cluster)
-        cluster_send(&inbox[rank], &stat_bar, tid, make_float4(st.m, st.s.hi, st.s.lo, failed ? 1.0f : 0.0f));
-      if (!cluster_receive(&stat_bar)) {
-        off = true;
-        status_set(a.status, THD_ERR_TIMEOUT);
-      }
-      float m = inbox[0].x;
-      for (int c = 1; c < cluster; ++c) m = fmaxf(m, inbox[c].x);
-      Pair s = {0.0f, 0.0f};
-      for (int c = 0; c < cluster; ++c) {
-        off |= inbox[c].w != 0.0f;
-        s = add(s, rescaled(inbox[c].x, {inbox[c].y, inbox[c].z}, m, a.scale));
-      }
-      st = {m, s};
+  } else {
+  // ---- the rows
+  int32_t b = 0, k = 0;
+  uint32_t phase = 0, active = 0;  // active: rows exchanged with the cluster
+  for (;; ++k) {
+    // a warp that finds the job there after another gave up waiting for it
+    // gives up too: all of them meet at the barriers below
+    bool ok = wait_or_quit(&job_full[k & 1], (k >> 1) & 1, &quit) && !quit;
+    // read where they are needed: registers are for the sweeps
+    const RowHead& h = heads[k & 1];
+    const Slice& sl = jobs[k & 1].slice;
+    const int64_t t = jobs[k & 1].row;
+    if (ok && t < 0) break;
+    const uint4* const buf = ring + b * shape.vecs;
+    uint64_t* const got = full + b * shape.chunks;
+    uint64_t* const freed = empty + b * shape.chunks;
+
+    if (ok && !jobs[k & 1].fetched) {  // a row that takes no part
+      if (tid == 0 && rank == 0) write_idle_row<kMode>(a, t);
+      if (a.dlogits) zero_slice<T, kThreads>(static_cast<T*>(a.dlogits) + t * a.dstride, sl, a.vocab);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&job_empty[k & 1]);
+      continue;
     }
-    RowResult r;
-    r.st = st;
-    r.mass = mass;
-    r.failed = off;
-    r.g = {0.0f, 0.0f};
-    if (!off) {
-      if (kMode == ROW_SCORE) {
-        if (tid == 0 && rank == 0) write_score(a, t, h, st);
-      } else if (kMode == ROW_POLICY) {
-        r.g = policy_row(a, t, h, st, tid == 0 && rank == 0);
-      } else if (!stat_is_empty(st)) {
-        r.g.k = a.grad_scale * h.weight * a.scale.tau * mass / st.s.hi;
-      }
-    }
-    if (tid == 0) result = r;
-    if (off && loading)  // no block of the cluster writes; the copies have to land
-      for (int i = 0; i < chunks; ++i) mbar_wait(&bars[i], 0);
-  }
-  if (kMode == ROW_SCORE) return;
-  __syncthreads();
-  const RowResult r = result;
-  if (r.failed) return;
-  const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + sl.count * N;  // the slice's elements
-  const auto mine = [&](int32_t id) {
-    return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
-           (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
-  };
-  EntryFix<kThreads> fix;
-  if (kMode == ROW_DISTILL) {
-    const T* held = reinterpret_cast<const T*>(buf);
-    const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
-    float part = teacher_entries<kThreads>(a, te, h.weight, r, mine, logit, fix);
-    part = block_sum(part, maxima);
-    if (cluster > 1) {
-      if (tid == 0) cluster_send(&loss_box[rank], &loss_bar, 0, make_float4(part, 0.0f, 0.0f, 0.0f));
-    } else if (tid == 0) {
-      a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
-    }
-  }
-  if (dz) {
-    const float shift = softmax_shift(r.st.m);
-    const uint64_t neg = pack2(-shift, -shift), hi = pack2(a.scale.hi, a.scale.hi), k2 = pack2(r.g.k, r.g.k);
-    const auto gradient = [&](const uint4& v) {
-      uint4 d;
-#pragma unroll
-      for (int j = 0; j < Word<T>::kPairs; ++j)
-        Word<T>::set_pair(d, j, mul2(k2, ex2_2(mul2(add2(Word<T>::pair(v, j), neg), hi))));
-      return d;
-    };
-    T* dv = dz + lo_v;
-    if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+
+    const int32_t count = ok ? sl.count : 0;
+    float edge = -INFINITY;
+    if (ok && tid < sl.edge_count)
+      edge = to_float(static_cast<const T*>(a.logits)[t * a.stride + edge_index(sl, tid, a.vocab)]);
+    // the slice's maximum, chunk by chunk as they land
+    uint32_t packed = kNone;
+    {
       const uint4* from = buf + tid;
-      uint4* to = reinterpret_cast<uint4*>(dv) + tid;
-      int32_t left = sl.count - tid;
-      for (; left > kStep - kThreads; left -= kStep, from += kStep, to += kStep) {
-        uint4 v[kVecsPerStep];
+      int32_t left = count - wid * 32;  // vectors from the warp's first one on
+      for (int j = 0; ok && j < shape.chunks; ++j, from += kChunk, left -= kChunk) {
+        ok = wait_or_quit(&got[j], phase, &quit);
+        if (left >= kChunk) {
 #pragma unroll
-        for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
-#pragma unroll
-        for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = gradient(v[u]);
-      }
-      for (; left > 0; left -= kThreads, from += kThreads, to += kThreads) *to = gradient(*from);
-    } else {
-      // a gradient laid out to another alignment than the logits
-      for (int32_t i = tid; i < sl.count; i += kThreads) {
-        const uint4 d = gradient(buf[i]);
-#pragma unroll
-        for (int j = 0; j < N; ++j) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + j, d, j);
+          for (int u = 0; u < kVecsPerStep * kChunkSteps; ++u) packed = max_vector<T>(packed, from[u * kThreads]);
+        } else {
+          for (int u = 0; u * kThreads < left; ++u)
+            if (lane < left - u * kThreads) packed = max_vector<T>(packed, from[u * kThreads]);
+        }
       }
     }
-    if (tid < sl.edge_count) {
-      const int32_t e = edge_index(sl, tid, a.vocab);
-      dz[e] = from_float<T>(r.g.k * ex2((to_float(z[e]) - shift) * a.scale.hi));
+    const float top = warp_max_one(fmaxf(Word<T>::top(packed), edge));
+    if (lane == 0) maxima[wid] = ok ? top : NAN;  // NaN: this warp gave up
+    group_sync<kThreads>();
+    float m = maxima[0];
+    ok = m == m;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      ok &= maxima[w] == maxima[w];
+      m = fmaxf(m, maxima[w]);
     }
-    if (kMode == ROW_POLICY && mine(h.label)) {
-      // over the value just written, by the thread that wrote it
-      const int32_t in = h.label - lo_v;
-      int32_t writer = in / N % kThreads;
-      if (in < 0) writer = h.label;                                        // the head
-      else if (h.label >= hi_v) writer = sl.edge_count - (a.vocab - h.label);  // the tail
-      if (tid == writer) dz[h.label] = from_float<T>(r.g.at_label);
+
+    if (!ok) {  // in every warp: a wait ran out, or the block was told to quit
+      if (wid == 0) {
+        if (cluster > 1 && lane < cluster)
+          cluster_send(&inbox[active & 1u][rank], &stat_bar[active & 1u], lane, make_float4(0.0f, 0.0f, 0.0f, 1.0f));
+        if (lane == 0) {
+          status_set(a.status, THD_ERR_TIMEOUT);
+          quit = 1;
+        }
+      }
+      break;
     }
-    if (kMode == ROW_DISTILL) {
-      __syncthreads();  // after the block's own values of the row
-      write_entries<T, kThreads>(a, te, dz, mine, fix);
+
+    // its sum of exponentials
+    {
+      ExpSum sum(softmax_shift(m));
+      const uint4* from = buf + tid;
+      int32_t left = count - wid * 32;
+      for (int j = 0; j < shape.chunks; ++j) {
+#pragma unroll
+        for (int q = 0; q < kChunkSteps; ++q, from += kStep, left -= kStep) {
+          if (left >= kStep) {
+            uint4 v[kVecsPerStep];
+#pragma unroll
+            for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
+#pragma unroll
+            for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], a.scale);
+          } else {
+#pragma unroll 1
+            for (int u = 0; u * kThreads < left; ++u)
+              sum.template add<T>(
+                  lane < left - u * kThreads ? from[u * kThreads] : make_uint4(kNone, kNone, kNone, kNone), a.scale);
+          }
+        }
+        if (kMode == ROW_SCORE) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&freed[j]);
+        }
+      }
+      float part = sum.total();
+      if (tid < sl.edge_count) part += exp_scaled(edge - softmax_shift(m), a.scale);
+      part = warp_sum(part);
+      if (lane == 0) parts[active & 1u][wid] = part;
+    }
+    group_sync<kThreads>();
+    if (wid == 0) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += parts[active & 1u][w];
+      SoftmaxStat st = {m, unbiased_sum(s)};
+      bool off = !wait_or_quit(&head_full[k & 1], (k >> 1) & 1, &quit);
+      if (cluster > 1) {
+        const uint32_t box = active & 1u;
+        __syncwarp();
+        if (lane < cluster)
+          cluster_send(&inbox[box][rank], &stat_bar[box], lane, make_float4(st.m, st.s.hi, st.s.lo, off ? 1.0f : 0.0f));
+        off |= !cluster_receive(&stat_bar[box], (active >> 1) & 1u);
+        // one block's statistics a lane
+        const float4 in = lane < cluster ? inbox[box][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        off = __any_sync(kFullMask, off || in.w != 0.0f);
+        st.m = warp_max_one(in.x);
+        Pair s = rescaled(in.x, {in.y, in.z}, st.m, a.scale);
+#pragma unroll
+        for (int o = kMaxCluster / 2; o > 0; o >>= 1)
+          s = add(s, {__shfl_xor_sync(kFullMask, s.hi, o), __shfl_xor_sync(kFullMask, s.lo, o)});
+        st.s = {__shfl_sync(kFullMask, s.hi, 0), __shfl_sync(kFullMask, s.lo, 0)};
+        if (lane == 0) mbar_arrive_expect_tx(&stat_bar[box], 16 * cluster);  // for the row after the next
+      }
+      RowResult r;
+      r.st = st;
+      r.g = {0.0f, 0.0f};
+      r.stop = off;
+      r.idle = !off && h.weight == 0.0f;  // a label out of range
+      if (r.idle) {
+        if (lane == 0 && rank == 0) write_idle_row<kMode>(a, t);
+      } else if (!off) {
+        r.g = finish_row<kMode>(a, t, h, st, lane == 0 && rank == 0);
+      }
+      if (lane == 0) {
+        result = r;
+        if (off) {
+          status_set(a.status, THD_ERR_TIMEOUT);
+          quit = 1;
+        }
+      }
+    }
+
+    if (kMode != ROW_SCORE) {
+      group_sync<kThreads>();
+      if (result.stop) break;  // no block of the cluster writes any more
+      const RowResult r = result;
+      const uint32_t box = active & 1u, box_phase = (active >> 1) & 1u;
+      const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + count * N;  // the slice's elements
+      const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
+      T* const dz = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
+      const auto mine = [&](int32_t id) {
+        return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
+               (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
+      };
+      const Teacher te = teacher_at(teachers + (k & 1) * teacher_bytes(a.teacher_count), a.teacher_count);
+      EntryFix<kThreads> fix;
+      if (kMode == ROW_DISTILL) {
+        const T* held = reinterpret_cast<const T*>(buf);
+        const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
+        // the first warp has waited for the entries; the barrier above orders the others after it
+        float part = teacher_entries<kThreads>(a, te, h, r, mine, logit, fix);
+        part = group_sum<kThreads>(part, parts[box]);
+        if (cluster > 1) {
+          if (tid == 0) cluster_send(&loss_box[box][rank], &loss_bar[box], 0, make_float4(part, 0.0f, 0.0f, 0.0f));
+        } else if (tid == 0) {
+          a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
+        }
+      }
+      const Gradient grad(softmax_shift(r.st.m), r.g.k);
+      T* const dv = dz + lo_v;
+      if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+        const uint4* from = buf + tid;
+        uint4* to = reinterpret_cast<uint4*>(dv) + tid;
+        int32_t left = count - wid * 32;
+        for (int j = 0; j < shape.chunks; ++j) {
+#pragma unroll
+          for (int q = 0; q < kChunkSteps; ++q, from += kStep, to += kStep, left -= kStep) {
+            if (left >= kStep) {
+              uint4 v[kVecsPerStep];
+#pragma unroll
+              for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
+#pragma unroll
+              for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = grad.template of<T>(v[u], a.scale);
+            } else {
+#pragma unroll 1
+              for (int u = 0; u * kThreads < left; ++u)
+                if (lane < left - u * kThreads) to[u * kThreads] = grad.template of<T>(from[u * kThreads], a.scale);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&freed[j]);
+        }
+      } else {
+        // no gradient, zeros, or one laid out to another alignment than the logits
+        if (dz && r.idle) {
+          zero_slice<T, kThreads>(dz, sl, a.vocab);
+        } else if (dz) {
+          for (int32_t i = tid; i < count; i += kThreads) {
+            const uint4 d = grad.template of<T>(buf[i], a.scale);
+#pragma unroll
+            for (int e = 0; e < N; ++e) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + e, d, e);
+          }
+        }
+        __syncwarp();
+        if (lane == 0)
+          for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&freed[j]);
+      }
+      if (dz && !r.idle) {
+        if (tid < sl.edge_count) dz[edge_index(sl, tid, a.vocab)] = from_float<T>(grad.of(edge, a.scale));
+        if (kMode == ROW_POLICY && mine(h.label)) {
+          // over the value just written, by the thread that wrote it
+          const int32_t in = h.label - lo_v;
+          int32_t writer = in / N % kThreads;
+          if (in < 0) writer = h.label;                                            // the head
+          else if (h.label >= hi_v) writer = sl.edge_count - (a.vocab - h.label);  // the tail
+          if (tid == writer) dz[h.label] = from_float<T>(r.g.at_label);
+        }
+        if (kMode == ROW_DISTILL) {
+          group_sync<kThreads>();  // after the block's own values of the row
+          write_entries<T, kThreads>(a, te, dz, mine, fix);
+        }
+      }
+      if (kMode == ROW_DISTILL && cluster > 1 && rank == 0 && tid == 0) {
+        if (!cluster_receive(&loss_bar[box], box_phase)) {
+          status_set(a.status, THD_ERR_TIMEOUT);
+        } else {
+          float part = 0.0f;
+          for (int c = 0; c < cluster; ++c) part += loss_box[box][c].x;
+          a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
+          mbar_arrive_expect_tx(&loss_bar[box], 16 * cluster);
+        }
+      }
+    }
+    ++active;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&job_empty[k & 1]);
+    if (++b == shape.buffers) {
+      b = 0;
+      phase ^= 1u;
     }
   }
-  if (kMode == ROW_DISTILL && cluster > 1 && rank == 0 && tid == 0) {
-    if (!cluster_receive(&loss_bar)) {
-      status_set(a.status, THD_ERR_TIMEOUT);
-      return;
-    }
-    float part = 0.0f;
-    for (int c = 0; c < cluster; ++c) part += loss_box[c].x;
-    a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
   }
+  // no block ends while another may still send to it
+  if (cluster > 1) cluster_sync();
 }
 
 // ---------------------------------------------------------------------------
@@ -624,68 +879,57 @@ __global__ void __launch_bounds__(kThreads) row_cluster_kernel(const __grid_cons
 
 constexpr int kPlainThreads = 512;
 
-// One block a row; the logits are read twice from memory, element by element.
+// One block a row; the logits are read three times from memory, element by
+// element.
 template <typename T, int kMode>
 __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_constant__ RowArgs a) {
-  extern __shared__ __align__(128) unsigned char dynamic[];
-  __shared__ float maxima[kPlainThreads / 32];
-  __shared__ Pair sums[kPlainThreads / 32];
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ float maxima[kPlainThreads / 32], parts[kPlainThreads / 32];
   __shared__ RowHead head;
   __shared__ RowResult result;
   __shared__ int32_t stop;
   pdl_wait_then_release();
   const int64_t t = blockIdx.x;
-  if (threadIdx.x == 0) {
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
     stop = status_load(a.status);
     if (!stop) head = row_head<T, kMode>(a, t);
   }
   __syncthreads();
   if (stop) return;
-  const RowHead h = head;
+  RowHead h = head;
   const T* z = static_cast<const T*>(a.logits) + t * a.stride;
   T* dz = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
   const uint32_t V = a.vocab, step = kPlainThreads;
   if (h.weight == 0.0f) {
-    if (threadIdx.x == 0) write_idle_row<kMode>(a, t);
+    if (tid == 0) write_idle_row<kMode>(a, t);
     if (dz)
-      for (uint32_t v = threadIdx.x; v < V; v += step) dz[v] = from_float<T>(0.0f);
+      for (uint32_t v = tid; v < V; v += step) dz[v] = from_float<T>(0.0f);
     return;
   }
   const Teacher te = teacher_at(dynamic, a.teacher_count);
-  float mass = 0.0f;
-  if (kMode == ROW_DISTILL && threadIdx.x < 32) mass = load_teacher(a, t, te, true);
-  ThreadStat ts;
-  constexpr int kBatch = 16;
-  for (uint32_t v0 = threadIdx.x; v0 < V; v0 += kBatch * step) {
-    float x[kBatch], top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const uint32_t v = v0 + i * step;
-      x[i] = v < V ? to_float(z[v]) : -INFINITY;
-      top = fmaxf(top, x[i]);
-    }
-    ts.raise(top, a.scale);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) sum += exp_scaled(x[i] - softmax_shift(ts.m), a.scale);
-    ts.s.hi += sum;
+  if (kMode == ROW_DISTILL && wid == 0) {
+    h.mass = load_teacher(a, t, te, true);
+    if (lane == 0) head.mass = h.mass;
   }
-  bool failed = false;
-  const SoftmaxStat st = block_stat(ts, a.scale, maxima, sums, &failed);
-  if (threadIdx.x < 32) {
+  float m = -INFINITY;
+#pragma unroll 8
+  for (uint32_t v = tid; v < V; v += step) m = fmaxf(m, to_float(z[v]));
+  m = warp_max_one(m);
+  if (lane == 0) maxima[wid] = m;
+  __syncthreads();
+  h.mass = head.mass;
+  for (int w = 0; w < kPlainThreads / 32; ++w) m = fmaxf(m, maxima[w]);
+  float s = 0.0f;
+#pragma unroll 8
+  for (uint32_t v = tid; v < V; v += step) s += exp_scaled(to_float(z[v]) - softmax_shift(m), a.scale);
+  const SoftmaxStat st = {m, unbiased_sum(group_sum<kPlainThreads>(s, parts))};
+  if (wid == 0) {
     RowResult r;
     r.st = st;
-    r.mass = mass;
-    r.failed = false;
-    r.g = {0.0f, 0.0f};
-    if (kMode == ROW_SCORE) {
-      if (threadIdx.x == 0) write_score(a, t, h, st);
-    } else if (kMode == ROW_POLICY) {
-      r.g = policy_row(a, t, h, st, threadIdx.x == 0);
-    } else if (!stat_is_empty(st)) {
-      r.g.k = a.grad_scale * h.weight * a.scale.tau * mass / st.s.hi;
-    }
-    if (threadIdx.x == 0) result = r;
+    r.g = finish_row<kMode>(a, t, h, st, lane == 0);
+    r.stop = r.idle = false;
+    if (lane == 0) result = r;
   }
   if (kMode == ROW_SCORE) return;
   __syncthreads();
@@ -694,14 +938,14 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   EntryFix<kPlainThreads> fix;
   if (kMode == ROW_DISTILL) {
     const auto logit = [&](int32_t id) { return to_float(z[id]); };
-    const float part = block_sum(teacher_entries<kPlainThreads>(a, te, h.weight, r, all, logit, fix), maxima);
-    if (threadIdx.x == 0) a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
+    const float part = group_sum<kPlainThreads>(teacher_entries<kPlainThreads>(a, te, h, r, all, logit, fix), parts);
+    if (tid == 0) a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
   }
   if (!dz) return;
   __syncthreads();  // every entry's logit is read before the gradient may take its place
-  const float shift = softmax_shift(r.st.m);
-  for (uint32_t v = threadIdx.x; v < V; v += step) {
-    float d = r.g.k * ex2((to_float(z[v]) - shift) * a.scale.hi);
+  const Gradient grad(softmax_shift(r.st.m), r.g.k);
+  for (uint32_t v = tid; v < V; v += step) {
+    float d = grad.of(to_float(z[v]), a.scale);
     if (kMode == ROW_POLICY && static_cast<int32_t>(v) == h.label) d = r.g.at_label;
     dz[v] = from_float<T>(d);
   }
@@ -717,23 +961,26 @@ thd_status_t done(cudaError_t e) {
   return THD_ERR_CUDA;
 }
 
-// Slices of about kSlice bytes let three blocks share an SM, each in a phase
-// of its own: one loads while another writes.
-constexpr int64_t kSlice = 76 * 1024;
+// Shared memory of an SM and what a block takes of it besides its buffers.
+constexpr int64_t kSmShared = 228 * 1024;
+constexpr int64_t kBlockShared = 1024 + 832;  // the driver's 1 KiB and the static arrays
+// Three blocks share an SM, each in a phase of its own: one waits for its
+// logits or its cluster while another computes or writes.
+constexpr int64_t kBlockBudget = kSmShared / 3 - kBlockShared;
 // Below this a slice is not divided further for want of rows.
 constexpr int64_t kSmallestSlice = 8 * 1024;
 
-template <typename T, int kMode, int kThreads>
-cudaError_t launch_cluster(const RowArgs& a, int32_t cluster, size_t smem, cudaStream_t s) {
-  auto* kernel = row_cluster_kernel<T, kMode, kThreads>;
+template <typename T, int kMode, int kWarps>
+cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaStream_t s) {
+  auto* kernel = row_cluster_kernel<T, kMode, kWarps>;
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
+  const int32_t cluster = 1 << shape.cluster_log2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.rows) * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kWarps * 32 + 64);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -745,29 +992,42 @@ cudaError_t launch_cluster(const RowArgs& a, int32_t cluster, size_t smem, cudaS
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  int32_t cluster_log2 = 0;
-  while ((1 << cluster_log2) < cluster) ++cluster_log2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, cluster_log2);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) << shape.cluster_log2);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, shape);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <typename T, int kMode>
 thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
-  const size_t entries = kMode == ROW_DISTILL ? teacher_bytes(a.teacher_count) : 0;
+  const int64_t entries = kMode == ROW_DISTILL ? 2 * static_cast<int64_t>(teacher_bytes(a.teacher_count)) : 0;
   const int sms = sm_count();
-  int32_t cluster = 1;
-  while (cluster < kMaxCluster && row > kSlice * cluster) cluster *= 2;
-  while (cluster < kMaxCluster && a.rows * static_cast<int64_t>(cluster) < sms && row > 2 * kSmallestSlice * cluster)
-    cluster *= 2;
-  const int64_t vecs = (row + 15) / 16;
-  const int64_t slice = (vecs + cluster - 1) / cluster * 16;
-  if (slice + static_cast<int64_t>(entries) > kMaxSlice || a.rows * static_cast<int64_t>(cluster) > INT32_MAX)
-    return done(launch_pdl(row_plain_kernel<T, kMode>, dim3(static_cast<unsigned>(a.rows)), dim3(kPlainThreads), entries,
-                           s, a));
-  const size_t smem = static_cast<size_t>(slice) + entries;
-  if (slice <= 8 * 1024) return done(launch_cluster<T, kMode, 128>(a, cluster, smem, s));
-  return done(launch_cluster<T, kMode, 256>(a, cluster, smem, s));
+  // vectors of a block's slice when a cluster of 2^k shares the row
+  const auto slice_of = [&](int32_t k) { return ((row + 15) / 16 + (int64_t(1) << k) - 1) >> k; };
+  RingShape shape;
+  shape.cluster_log2 = 0;
+  while ((1 << shape.cluster_log2) < kMaxCluster && slice_of(shape.cluster_log2) * 16 + entries > kBlockBudget)
+    ++shape.cluster_log2;
+  while ((1 << shape.cluster_log2) < kMaxCluster && (static_cast<int64_t>(a.rows) << shape.cluster_log2) < sms &&
+         slice_of(shape.cluster_log2) * 16 > 2 * kSmallestSlice)
+    ++shape.cluster_log2;
+  const int64_t slice = slice_of(shape.cluster_log2);
+  if (slice * 16 + entries > kMaxSlice || static_cast<int64_t>(a.rows) << shape.cluster_log2 > INT32_MAX)
+    return done(launch_pdl(row_plain_kernel<T, kMode>, dim3(static_cast<unsigned>(a.rows)), dim3(kPlainThreads),
+                           static_cast<size_t>(entries / 2), s, a));
+#ifdef EXP_WARPS
+  const int warps = slice <= 512 ? 4 : EXP_WARPS;
+#else
+  const int warps = slice <= 512 ? 4 : 8;
+#endif
+  const int64_t step = warps * 32 * kVecsPerStep * kChunkSteps;
+  shape.vecs = static_cast<int32_t>(slice);
+  shape.chunks = static_cast<int32_t>(std::max<int64_t>(1, (slice + step - 1) / step));
+  const int64_t fit = (kBlockBudget / (slice <= 512 ? 4 : 1) - entries) / std::max<int64_t>(16, slice * 16);
+  shape.buffers = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fit, kMaxChunks / shape.chunks)));
+  const size_t smem = static_cast<size_t>(shape.buffers * slice * 16 + entries);
+  if (warps == 4) return done(launch_cluster<T, kMode, 4>(a, shape, smem, s));
+  return done(launch_cluster<T, kMode, 8>(a, shape, smem, s));
 }
 
 template <typename T>
@@ -825,14 +1085,8 @@ __global__ void __launch_bounds__(kBackThreads)
   }
   const float z_label = tid == writer ? to_float(z[label]) : 0.0f;
 
-  const uint64_t neg = pack2(-top, -top), hi = pack2(a.scale.hi, a.scale.hi), k2 = pack2(k, k);
-  const auto gradient = [&](const uint4& v) {
-    uint4 d;
-#pragma unroll
-    for (int j = 0; j < Word<T>::kPairs; ++j)
-      Word<T>::set_pair(d, j, mul2(k2, ex2_2(mul2(add2(Word<T>::pair(v, j), neg), hi))));
-    return d;
-  };
+  const Gradient grad(top, k);
+  const auto gradient = [&](const uint4& v) { return grad.of<T>(v, a.scale); };
   const uint4 zeros = make_uint4(0, 0, 0, 0);
   T* dv = dz + lo_v;
   if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
@@ -859,7 +1113,7 @@ __global__ void __launch_bounds__(kBackThreads)
   }
   if (tile == 0 && tid < row.edge_count) {
     const int32_t e = edge_index(row, tid, a.vocab);
-    dz[e] = from_float<T>(idle ? 0.0f : k * ex2((to_float(z[e]) - top) * a.scale.hi));
+    dz[e] = from_float<T>(idle ? 0.0f : grad.of(to_float(z[e]), a.scale));
   }
   if (tid == writer) dz[label] = from_float<T>(g + k * exp_scaled(z_label - top, a.scale));
 }
