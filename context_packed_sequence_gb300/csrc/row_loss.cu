@@ -225,46 +225,32 @@ struct RowResult {
   bool idle;  // the row takes no part after all
 };
 
-// kThreads threads; every entry of the teacher is some thread's.
-template <int kThreads>
-struct EntryFix {
-  static constexpr int kPer = (kMaxTeacher + kThreads - 1) / kThreads;
-  float at[kPer];  // gradient in the entry's place
-};
-
-// Loss terms of the entries for which `mine(id)` and their gradients;
-// `logit(id)` reads the row.  Returns this thread's part of the loss / tau^2.
-template <int kThreads, class Mine, class Logit>
-__device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher& te, const RowHead& h,
-                                                 const RowResult& r, Mine mine, Logit logit,
-                                                 EntryFix<kThreads>& fix) {
-  const RowNorm norm = row_norm(r.st);
+// The loss terms of the teacher's entries for which `mine(id)`, entry by entry
+// from `first` in steps of `step`; `logit(id)` reads the row.  Leaves the
+// gradient in the entry's place in te.lq and returns the loss / tau^2.
+template <class Mine, class Logit>
+__device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher& te, const RowHead& h, SoftmaxStat st,
+                                                 int32_t first, int32_t step, Mine mine, Logit logit) {
+  const RowNorm norm = row_norm(st);
   const float gs = a.grad_scale * h.weight * a.scale.tau;
-  const bool empty = stat_is_empty(r.st);
+  const bool empty = stat_is_empty(st);
   float loss = 0.0f;
-#pragma unroll
-  for (int j = 0; j < EntryFix<kThreads>::kPer; ++j) {
-    const int k = threadIdx.x + j * kThreads;
-    fix.at[j] = 0.0f;
-    if (k >= a.teacher_count) break;
+  for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
     if (id < 0 || !mine(id)) continue;
     const Pair lp = entry_logprob(logit(id), empty, norm, a.scale);
     if (te.q[k] != 0.0f) loss += te.q[k] * ((te.lq[k] - lp.hi) - lp.lo);
-    fix.at[j] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
+    te.lq[k] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
   }
   return loss;
 }
 
-template <typename T, int kThreads, class Mine>
-__device__ __forceinline__ void write_entries(const RowArgs& a, const Teacher& te, T* dz, Mine mine,
-                                              const EntryFix<kThreads>& fix) {
-#pragma unroll
-  for (int j = 0; j < EntryFix<kThreads>::kPer; ++j) {
-    const int k = threadIdx.x + j * kThreads;
-    if (k >= a.teacher_count) break;
+template <typename T, class Mine>
+__device__ __forceinline__ void write_entries(const RowArgs& a, const Teacher& te, T* dz, int32_t first, int32_t step,
+                                              Mine mine) {
+  for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
-    if (id >= 0 && mine(id)) dz[id] = from_float<T>(fix.at[j]);
+    if (id >= 0 && mine(id)) dz[id] = from_float<T>(te.lq[k]);
   }
 }
 
@@ -297,8 +283,7 @@ __device__ __forceinline__ RowGrad finish_row(const RowArgs& a, int64_t t, const
 // rows shared by a cluster
 // ---------------------------------------------------------------------------
 
-constexpr int kVecsPerStep = 4;  // vectors a thread holds in registers at a time
-constexpr int kChunkSteps = 2;   // steps in a part of a slice that arrives on its own
+constexpr int kVecsPerStep = 8;  // vectors a thread holds in registers at a time: a chunk is a step of the block
 constexpr int kMaxChunks = 8;    // chunks of all buffers
 constexpr int kMaxCluster = 8;   // largest portable cluster
 constexpr int kMaxSlice = 208 * 1024;
@@ -397,14 +382,13 @@ struct Slice {
 };
 
 template <typename T>
-__device__ __forceinline__ Slice row_slice(const T* z, int32_t V, int32_t rank, int32_t cluster_log2) {
+__device__ __forceinline__ Slice row_slice(const T* z, int32_t V, int32_t rank, int32_t cluster) {
   constexpr int N = Word<T>::kElems;
   Slice s;
   const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) & 15u);
   s.head = min(V, static_cast<int32_t>(((16u - mis) & 15u) / sizeof(T)));
-  const int32_t cluster = 1 << cluster_log2;
   const int32_t vecs = static_cast<int32_t>(static_cast<uint32_t>(V - s.head) / N);
-  const int32_t per = (vecs + cluster - 1) >> cluster_log2;
+  const int32_t per = static_cast<int32_t>(static_cast<uint32_t>(vecs + cluster - 1) / static_cast<uint32_t>(cluster));
   s.first = min(vecs, rank * per);
   s.count = min(vecs, s.first + per) - s.first;
   const int32_t tail = s.head + vecs * N;
@@ -444,7 +428,7 @@ __device__ __forceinline__ void zero_slice(T* dz, const Slice& sl, int32_t V) {
 
 // How a launch lays out its blocks' shared memory.
 struct RingShape {
-  int32_t cluster_log2;
+  int32_t cluster;  // blocks of a cluster, 1 .. kMaxCluster
   int32_t buffers;  // row slices held at a time
   int32_t chunks;   // chunks of a slice (the last ones may be empty)
   int32_t vecs;     // vectors a buffer holds
@@ -489,13 +473,12 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
     row_cluster_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
   constexpr int N = Word<T>::kElems;
   constexpr int kThreads = kWarps * 32;
-  constexpr int kStep = kThreads * kVecsPerStep;  // vectors of a step
-  constexpr int kChunk = kStep * kChunkSteps;     // vectors of a chunk
+  constexpr int kChunk = kThreads * kVecsPerStep;  // vectors of a chunk
   constexpr uint32_t kNone = Word<T>::kNegInf;
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ uint64_t full[kMaxChunks], empty[kMaxChunks];    // of each chunk of each buffer
   __shared__ uint64_t job_full[2], job_empty[2], head_full[2], stat_bar[2], next_full[2], next_free[2];
-  __shared__ uint64_t loss_bar[kMode == ROW_DISTILL ? 2 : 1];
+  __shared__ uint64_t loss_bar[2], result_full[2], written[2];  // ROW_DISTILL
   __shared__ float maxima[kWarps], parts[2][kWarps];
   __shared__ __align__(16) float4 next[2];                    // answers to requests for rows
   __shared__ __align__(16) float4 inbox[2][kMaxCluster];      // each block's statistics of a row
@@ -503,18 +486,18 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
   __shared__ __align__(16) float4 loss_box[kMode == ROW_DISTILL ? 2 : 1][kMode == ROW_DISTILL ? kMaxCluster : 1];
   __shared__ RowJob jobs[2];
   __shared__ RowHead heads[2];
-  __shared__ RowResult result;
+  __shared__ RowResult results[2];
   __shared__ volatile int32_t quit;
   __shared__ int32_t stop;
 
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
-  const int32_t cluster = 1 << shape.cluster_log2;
+  const int32_t cluster = shape.cluster;
   const int32_t rank = cluster > 1 ? static_cast<int32_t>(cluster_rank()) : 0;
   if (tid == 0) {
     quit = 0;
     for (int i = 0; i < shape.buffers * shape.chunks; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
+      mbar_init(&empty[i], kMode == ROW_DISTILL ? kWarps + 1 : kWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&job_full[i], 1);
@@ -526,6 +509,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
       if (cluster > 1) mbar_arrive_expect_tx(&stat_bar[i], 16 * cluster);
       if (kMode == ROW_DISTILL) {
         mbar_init(&loss_bar[i], 1);
+        mbar_init(&result_full[i], 1);
+        mbar_init(&written[i], kWarps);
         if (cluster > 1 && rank == 0) mbar_arrive_expect_tx(&loss_bar[i], 16 * cluster);
       }
     }
@@ -577,8 +562,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
     }
   } else if (wid == kWarps + 1) {
     // ---- which rows, their scalars and teacher entries
-    int32_t row = static_cast<int32_t>(blockIdx.x >> shape.cluster_log2);
+    int32_t row = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(cluster));
     bool ok = true;
+    int32_t b = 0;        // ROW_DISTILL: buffer of the row before
+    uint32_t active = 0;  // and rows with entries so far
     for (int32_t k = 0; ok; ++k) {
       float weight = 0.0f;
       if (row >= 0) {
@@ -600,11 +587,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         RowJob job;
         job.row = row;
         job.fetched = weight != 0.0f;
-        job.slice = row_slice(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, shape.cluster_log2);
+        job.slice = row_slice(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, cluster);
         jobs[k & 1] = job;
         mbar_arrive(&job_full[k & 1]);
       }
-      if (row < 0) break;
       if (weight != 0.0f) {
         RowHead h;
         if (lane == 0) h = row_head<T, kMode>(a, row);
@@ -615,7 +601,51 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         if (lane == 0) heads[k & 1] = h;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&head_full[k & 1]);
+      if (row >= 0 && lane == 0) mbar_arrive(&head_full[k & 1]);
+      if (kMode == ROW_DISTILL && k > 0 && jobs[(k - 1) & 1].fetched) {
+        // ---- meanwhile the row before has its statistics: its entries
+        const int32_t before = (k - 1) & 1;
+        if (!(ok = wait_or_quit(&result_full[active & 1], (active >> 1) & 1, &quit))) break;
+        const RowResult r = results[before];
+        const RowHead& h = heads[before];
+        const Slice& sl = jobs[before].slice;
+        const int64_t t = jobs[before].row;
+        if (r.stop) break;
+        const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
+        const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + sl.count * N;  // the slice's elements
+        const auto mine = [&](int32_t id) {
+          return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
+                 (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
+        };
+        const Teacher te = teacher_at(teachers + before * teacher_bytes(a.teacher_count), a.teacher_count);
+        const T* held = reinterpret_cast<const T*>(ring + b * shape.vecs);
+        const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
+        const float part = warp_sum(teacher_entries(a, te, h, r.st, lane, 32, mine, logit));
+        __syncwarp();
+        if (lane == 0)
+          for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&empty[b * shape.chunks + j]);
+        if (++b == shape.buffers) b = 0;
+        const uint32_t box = active & 1;
+        if (cluster > 1 && lane == 0)
+          cluster_send(&loss_box[box][rank], &loss_bar[box], 0, make_float4(part, 0.0f, 0.0f, 0.0f));
+        if (a.dlogits) {  // over the block's own values of the row
+          if (!(ok = wait_or_quit(&written[active & 1], (active >> 1) & 1, &quit))) break;
+          write_entries(a, te, static_cast<T*>(a.dlogits) + t * a.dstride, lane, 32, mine);
+        }
+        if (rank == 0 && lane == 0) {
+          float loss = part;
+          if (cluster > 1) {
+            if (!cluster_receive(&loss_bar[box], (active >> 1) & 1)) status_set(a.status, THD_ERR_TIMEOUT);
+            loss = 0.0f;
+            for (int c = 0; c < cluster; ++c) loss += loss_box[box][c].x;
+            mbar_arrive_expect_tx(&loss_bar[box], 16 * cluster);
+          }
+          a.token_losses[t] = loss * (a.scale.tau * a.scale.tau);
+        }
+        ++active;
+        __syncwarp();
+      }
+      if (row < 0) break;
       // the answer, which every block of the cluster gets
       const int i = (k + 1) & 1;
       if (!(ok = cluster_receive(&next_full[i], (k >> 1) & 1))) {
@@ -623,7 +653,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         break;
       }
       const int32_t block = requested_block(&next[i]);
-      row = block < 0 ? -1 : block >> shape.cluster_log2;
+      row = block < 0 ? -1 : static_cast<int32_t>(static_cast<uint32_t>(block) / static_cast<uint32_t>(cluster));
       __syncwarp();
       if (lane == 0) cluster_arrive0(&next_free[i]);
     }
@@ -665,9 +695,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         ok = wait_or_quit(&got[j], phase, &quit);
         if (left >= kChunk) {
 #pragma unroll
-          for (int u = 0; u < kVecsPerStep * kChunkSteps; ++u) packed = max_vector<T>(packed, from[u * kThreads]);
+          for (int u = 0; u < kVecsPerStep; ++u) packed = max_vector<T>(packed, from[u * kThreads]);
         } else {
-          for (int u = 0; u * kThreads < left; ++u)
+#pragma unroll
+          for (int u = 0; u < kVecsPerStep; ++u)
             if (lane < left - u * kThreads) packed = max_vector<T>(packed, from[u * kThreads]);
         }
       }
@@ -700,21 +731,18 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
       ExpSum sum(softmax_shift(m));
       const uint4* from = buf + tid;
       int32_t left = count - wid * 32;
-      for (int j = 0; j < shape.chunks; ++j) {
+      for (int j = 0; j < shape.chunks; ++j, from += kChunk, left -= kChunk) {
+        if (left >= kChunk) {
+          uint4 v[kVecsPerStep];
 #pragma unroll
-        for (int q = 0; q < kChunkSteps; ++q, from += kStep, left -= kStep) {
-          if (left >= kStep) {
-            uint4 v[kVecsPerStep];
+          for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
 #pragma unroll
-            for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
-#pragma unroll
-            for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], a.scale);
-          } else {
+          for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], a.scale);
+        } else {
 #pragma unroll 1
-            for (int u = 0; u * kThreads < left; ++u)
-              sum.template add<T>(
-                  lane < left - u * kThreads ? from[u * kThreads] : make_uint4(kNone, kNone, kNone, kNone), a.scale);
-          }
+          for (int u = 0; u * kThreads < left; ++u)
+            sum.template add<T>(
+                lane < left - u * kThreads ? from[u * kThreads] : make_uint4(kNone, kNone, kNone, kNone), a.scale);
         }
         if (kMode == ROW_SCORE) {
           __syncwarp();
@@ -761,7 +789,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         r.g = finish_row<kMode>(a, t, h, st, lane == 0 && rank == 0);
       }
       if (lane == 0) {
-        result = r;
+        results[k & 1] = r;
+        if (kMode == ROW_DISTILL) mbar_arrive(&result_full[active & 1u]);
         if (off) {
           status_set(a.status, THD_ERR_TIMEOUT);
           quit = 1;
@@ -771,9 +800,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
 
     if (kMode != ROW_SCORE) {
       group_sync<kThreads>();
-      if (result.stop) break;  // no block of the cluster writes any more
-      const RowResult r = result;
-      const uint32_t box = active & 1u, box_phase = (active >> 1) & 1u;
+      const RowResult r = results[k & 1];
+      if (r.stop) break;  // no block of the cluster writes any more
       const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + count * N;  // the slice's elements
       const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
       T* const dz = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
@@ -781,40 +809,23 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
                (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
       };
-      const Teacher te = teacher_at(teachers + (k & 1) * teacher_bytes(a.teacher_count), a.teacher_count);
-      EntryFix<kThreads> fix;
-      if (kMode == ROW_DISTILL) {
-        const T* held = reinterpret_cast<const T*>(buf);
-        const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
-        // the first warp has waited for the entries; the barrier above orders the others after it
-        float part = teacher_entries<kThreads>(a, te, h, r, mine, logit, fix);
-        part = group_sum<kThreads>(part, parts[box]);
-        if (cluster > 1) {
-          if (tid == 0) cluster_send(&loss_box[box][rank], &loss_bar[box], 0, make_float4(part, 0.0f, 0.0f, 0.0f));
-        } else if (tid == 0) {
-          a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
-        }
-      }
       const Gradient grad(softmax_shift(r.st.m), r.g.k);
       T* const dv = dz + lo_v;
       if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
         const uint4* from = buf + tid;
         uint4* to = reinterpret_cast<uint4*>(dv) + tid;
         int32_t left = count - wid * 32;
-        for (int j = 0; j < shape.chunks; ++j) {
+        for (int j = 0; j < shape.chunks; ++j, from += kChunk, to += kChunk, left -= kChunk) {
+          if (left >= kChunk) {
+            uint4 v[kVecsPerStep];
 #pragma unroll
-          for (int q = 0; q < kChunkSteps; ++q, from += kStep, to += kStep, left -= kStep) {
-            if (left >= kStep) {
-              uint4 v[kVecsPerStep];
+            for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
 #pragma unroll
-              for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
-#pragma unroll
-              for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = grad.template of<T>(v[u], a.scale);
-            } else {
+            for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = grad.template of<T>(v[u], a.scale);
+          } else {
 #pragma unroll 1
-              for (int u = 0; u * kThreads < left; ++u)
-                if (lane < left - u * kThreads) to[u * kThreads] = grad.template of<T>(from[u * kThreads], a.scale);
-            }
+            for (int u = 0; u * kThreads < left; ++u)
+              if (lane < left - u * kThreads) to[u * kThreads] = grad.template of<T>(from[u * kThreads], a.scale);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&freed[j]);
@@ -844,20 +855,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
           else if (h.label >= hi_v) writer = sl.edge_count - (a.vocab - h.label);  // the tail
           if (tid == writer) dz[h.label] = from_float<T>(r.g.at_label);
         }
-        if (kMode == ROW_DISTILL) {
-          group_sync<kThreads>();  // after the block's own values of the row
-          write_entries<T, kThreads>(a, te, dz, mine, fix);
-        }
       }
-      if (kMode == ROW_DISTILL && cluster > 1 && rank == 0 && tid == 0) {
-        if (!cluster_receive(&loss_bar[box], box_phase)) {
-          status_set(a.status, THD_ERR_TIMEOUT);
-        } else {
-          float part = 0.0f;
-          for (int c = 0; c < cluster; ++c) part += loss_box[box][c].x;
-          a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
-          mbar_arrive_expect_tx(&loss_bar[box], 16 * cluster);
-        }
+      if (kMode == ROW_DISTILL) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&written[active & 1u]);
       }
     }
     ++active;
@@ -935,10 +936,9 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   __syncthreads();
   const RowResult r = result;
   const auto all = [](int32_t) { return true; };
-  EntryFix<kPlainThreads> fix;
   if (kMode == ROW_DISTILL) {
     const auto logit = [&](int32_t id) { return to_float(z[id]); };
-    const float part = group_sum<kPlainThreads>(teacher_entries<kPlainThreads>(a, te, h, r, all, logit, fix), parts);
+    const float part = group_sum<kPlainThreads>(teacher_entries(a, te, h, r.st, tid, kPlainThreads, all, logit), parts);
     if (tid == 0) a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
   }
   if (!dz) return;
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   }
   if (kMode == ROW_DISTILL) {
     __syncthreads();  // after the block's own values of the row
-    write_entries<T, kPlainThreads>(a, te, dz, all, fix);
+    write_entries(a, te, dz, tid, kPlainThreads, all);
   }
 }
 
@@ -978,7 +978,7 @@ cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaS
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int32_t cluster = 1 << shape.cluster_log2;
+  const int32_t cluster = shape.cluster;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kWarps * 32 + 64);
   cfg.dynamicSmemBytes = smem;
@@ -992,7 +992,7 @@ cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaS
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) << shape.cluster_log2);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * cluster);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, shape);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -1002,28 +1002,23 @@ thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
   const int64_t entries = kMode == ROW_DISTILL ? 2 * static_cast<int64_t>(teacher_bytes(a.teacher_count)) : 0;
   const int sms = sm_count();
-  // vectors of a block's slice when a cluster of 2^k shares the row
-  const auto slice_of = [&](int32_t k) { return ((row + 15) / 16 + (int64_t(1) << k) - 1) >> k; };
+  // vectors of a block's slice when `cluster` blocks share the row
+  const auto slice_of = [&](int32_t cluster) { return ((row + 15) / 16 + cluster - 1) / cluster; };
   RingShape shape;
-  shape.cluster_log2 = 0;
-  while ((1 << shape.cluster_log2) < kMaxCluster && slice_of(shape.cluster_log2) * 16 + entries > kBlockBudget)
-    ++shape.cluster_log2;
-  while ((1 << shape.cluster_log2) < kMaxCluster && (static_cast<int64_t>(a.rows) << shape.cluster_log2) < sms &&
-         slice_of(shape.cluster_log2) * 16 > 2 * kSmallestSlice)
-    ++shape.cluster_log2;
-  const int64_t slice = slice_of(shape.cluster_log2);
-  if (slice * 16 + entries > kMaxSlice || static_cast<int64_t>(a.rows) << shape.cluster_log2 > INT32_MAX)
+  shape.cluster = 1;
+  while (shape.cluster < kMaxCluster && slice_of(shape.cluster) * 16 + entries > kBlockBudget) ++shape.cluster;
+  while (shape.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * (shape.cluster + 1) <= sms &&
+         slice_of(shape.cluster + 1) * 16 >= kSmallestSlice)
+    ++shape.cluster;
+  const int64_t slice = slice_of(shape.cluster);
+  if (slice * 16 + entries > kMaxSlice || static_cast<int64_t>(a.rows) * shape.cluster > INT32_MAX)
     return done(launch_pdl(row_plain_kernel<T, kMode>, dim3(static_cast<unsigned>(a.rows)), dim3(kPlainThreads),
                            static_cast<size_t>(entries / 2), s, a));
-#ifdef EXP_WARPS
-  const int warps = slice <= 512 ? 4 : EXP_WARPS;
-#else
   const int warps = slice <= 512 ? 4 : 8;
-#endif
-  const int64_t step = warps * 32 * kVecsPerStep * kChunkSteps;
+  const int64_t step = warps * 32 * kVecsPerStep;
   shape.vecs = static_cast<int32_t>(slice);
   shape.chunks = static_cast<int32_t>(std::max<int64_t>(1, (slice + step - 1) / step));
-  const int64_t fit = (kBlockBudget / (slice <= 512 ? 4 : 1) - entries) / std::max<int64_t>(16, slice * 16);
+  const int64_t fit = (kBlockBudget / (warps == 4 ? 4 : 1) - entries) / std::max<int64_t>(16, slice * 16);
   shape.buffers = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fit, kMaxChunks / shape.chunks)));
   const size_t smem = static_cast<size_t>(shape.buffers * slice * 16 + entries);
   if (warps == 4) return done(launch_cluster<T, kMode, 4>(a, shape, smem, s));
@@ -1063,7 +1058,7 @@ __global__ void __launch_bounds__(kBackThreads)
   if (status_load(a.status) != 0) return;
   const T* z = static_cast<const T*>(a.logits) + t * a.stride;
   T* dz = static_cast<T*>(a.dlogits) + t * a.dstride;
-  const Slice row = row_slice(z, a.vocab, 0, 0);
+  const Slice row = row_slice(z, a.vocab, 0, 1);
   const int32_t first = tile * kBackTile, count = min(kBackTile, row.count - first);
   const int32_t lo_v = row.head + first * N, hi_v = lo_v + max(count, 0) * N;
   const bool bad = up != 0.0f && (label < 0 || label >= a.vocab);
