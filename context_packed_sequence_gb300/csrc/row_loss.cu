@@ -11,6 +11,18 @@
 
 #include "loss_internal.cuh"
 
+#ifndef EXP_MINB
+#define EXP_MINB 3
+#endif
+#ifndef EXP_G
+#define EXP_G 4
+#endif
+#ifndef EXP_ROWS
+#define EXP_ROWS 1
+#endif
+#ifndef EXP_PER
+#define EXP_PER 3
+#endif
 namespace thd {
 namespace {
 
@@ -221,8 +233,9 @@ __device__ __forceinline__ void group_sync() {
 struct RowResult {
   SoftmaxStat st;
   RowGrad g;
-  bool stop;  // something failed: nothing more is written
-  bool idle;  // the row takes no part after all
+  int32_t writer;  // the thread that wrote the label's place and writes it again; -1: none here
+  bool stop;       // something failed: nothing more is written
+  bool idle;       // the row takes no part after all
 };
 
 // The loss terms of the teacher's entries for which `mine(id)`, entry by entry
@@ -283,10 +296,12 @@ __device__ __forceinline__ RowGrad finish_row(const RowArgs& a, int64_t t, const
 // rows shared by a cluster
 // ---------------------------------------------------------------------------
 
-constexpr int kVecsPerStep = 8;  // vectors a thread holds in registers at a time: a chunk is a step of the block
-constexpr int kMaxChunks = 8;    // chunks of all buffers
+constexpr int kVecsPerStep = 4;  // vectors a thread holds in registers at a time
+constexpr int kChunkSteps = 2;   // steps in a chunk, the part of a slice that arrives and is freed on its own
+constexpr int kMaxChunks = 16;   // chunks of all buffers
+constexpr int kJobs = 4;         // rows known at a time
 constexpr int kMaxCluster = 8;   // largest portable cluster
-constexpr int kMaxSlice = 208 * 1024;
+constexpr int kMaxSlice = 216 * 1024;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -345,16 +360,16 @@ __device__ __forceinline__ int32_t requested_block(const void* slot) {
   return got ? static_cast<int32_t>(x) : -1;
 }
 
-// A float4 into block `rank`'s shared memory, at this block's addresses of the
-// slot and of the barrier that counts its 16 bytes.
-__device__ __forceinline__ void cluster_send(const float4* at, const uint64_t* bar, uint32_t rank, float4 v) {
+// Two floats into block `rank`'s shared memory, at this block's addresses of
+// the slot and of the barrier that counts the 8 bytes.  Only in a launch with
+// clusters.
+__device__ __forceinline__ void cluster_send(const float2* at, const uint64_t* bar, uint32_t rank, float2 v) {
   uint32_t slot, counter;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(slot) : "r"(smem_addr(at)), "r"(rank));
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(counter) : "r"(smem_addr(bar)), "r"(rank));
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(slot),
-      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(counter)
-      : "memory");
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(slot),
+               "f"(v.x), "f"(v.y), "r"(counter)
+               : "memory");
 }
 // Bounded wait for what the cluster sends here (like mbar_wait).
 __device__ __forceinline__ bool cluster_receive(uint64_t* bar, uint32_t parity) {
@@ -429,6 +444,7 @@ __device__ __forceinline__ void zero_slice(T* dz, const Slice& sl, int32_t V) {
 // How a launch lays out its blocks' shared memory.
 struct RingShape {
   int32_t cluster;  // blocks of a cluster, 1 .. kMaxCluster
+  int32_t group;    // rows a cluster takes at a time, up to 32
   int32_t buffers;  // row slices held at a time
   int32_t chunks;   // chunks of a slice (the last ones may be empty)
   int32_t vecs;     // vectors a buffer holds
@@ -462,31 +478,41 @@ struct RowJob {
   Slice slice;
 };
 
-// The grid has a cluster for every row; those that run take the rows of those
-// that have not started, so a cluster's blocks stay for many rows and yet no
-// cluster is left with more than its share.  kWarps warps compute.  One more
-// fetches the slices into a ring of buffers, chunk by chunk as they become
-// free, and another finds the next row and reads what it needs besides its
-// logits, up to two rows ahead.
+// The grid has a cluster for every group of rows; those that run take the rows
+// of those that have not started, so a cluster's blocks stay for many rows and yet no
+// cluster is left with more than its share.
+//
+// kWarps warps compute: the statistics of a row's slice, then its gradient.
+// Three more serve them.  One finds the next rows and reads what they need
+// besides their logits.  One fetches the slices into a ring of buffers, chunk
+// by chunk as they become free.  One joins the statistics, which every warp of
+// every block of the cluster sends to every block, and finishes the row's
+// scalars and a teacher's entries.  No barrier of the block is waited at: a
+// warp that gives up waiting tells the others and leaves.
+//
+// Statistics of row n (rows with weight counted) go to box n % 2.  A warp
+// sends row n when its block has the result of row n - 1, so every block has
+// sent row n - 1, and had the result of row n - 2: that box has been read.
 template <typename T, int kMode, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
+__global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
     row_cluster_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
   constexpr int N = Word<T>::kElems;
   constexpr int kThreads = kWarps * 32;
-  constexpr int kChunk = kThreads * kVecsPerStep;  // vectors of a chunk
+  constexpr int kStep = kThreads * kVecsPerStep;  // vectors of a step
+  constexpr int kChunk = kStep * kChunkSteps;     // vectors of a chunk
   constexpr uint32_t kNone = Word<T>::kNegInf;
   extern __shared__ __align__(16) unsigned char dynamic[];
-  __shared__ uint64_t full[kMaxChunks], empty[kMaxChunks];    // of each chunk of each buffer
-  __shared__ uint64_t job_full[2], job_empty[2], head_full[2], stat_bar[2], next_full[2], next_free[2];
-  __shared__ uint64_t loss_bar[2], result_full[2], written[2];  // ROW_DISTILL
-  __shared__ float maxima[kWarps], parts[2][kWarps];
-  __shared__ __align__(16) float4 next[2];                    // answers to requests for rows
-  __shared__ __align__(16) float4 inbox[2][kMaxCluster];      // each block's statistics of a row
+  __shared__ uint64_t full[kMaxChunks], empty[kMaxChunks];  // of each chunk of each buffer
+  __shared__ uint64_t job_full[kJobs], job_empty[kJobs], head_full[kJobs], result_full[kJobs];
+  __shared__ uint64_t written[kMode == ROW_DISTILL ? kJobs : 1], loss_bar[kMode == ROW_DISTILL ? kJobs : 1];
+  __shared__ uint64_t stat_bar[2], next_full[2], next_free[2];
+  __shared__ __align__(16) float4 next[2];               // answers to requests for rows
+  __shared__ float2 inbox[2][kMaxCluster * kWarps];      // each warp's statistics of a row
   // each block's part of a distillation loss
-  __shared__ __align__(16) float4 loss_box[kMode == ROW_DISTILL ? 2 : 1][kMode == ROW_DISTILL ? kMaxCluster : 1];
-  __shared__ RowJob jobs[2];
-  __shared__ RowHead heads[2];
-  __shared__ RowResult results[2];
+  __shared__ float2 loss_box[kMode == ROW_DISTILL ? kJobs : 1][kMode == ROW_DISTILL ? kMaxCluster : 1];
+  __shared__ RowJob jobs[kJobs];
+  __shared__ RowHead heads[kJobs];
+  __shared__ RowResult results[kJobs];
   __shared__ volatile int32_t quit;
   __shared__ int32_t stop;
 
@@ -499,20 +525,22 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kMode == ROW_DISTILL ? kWarps + 1 : kWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kJobs; ++i) {
       mbar_init(&job_full[i], 1);
-      mbar_init(&job_empty[i], kWarps + 1);
+      mbar_init(&job_empty[i], kWarps + 2);
       mbar_init(&head_full[i], 1);
-      mbar_init(&stat_bar[i], 1);
+      mbar_init(&result_full[i], 1);
+      if (kMode == ROW_DISTILL) {
+        mbar_init(&written[i], kWarps);
+        mbar_init(&loss_bar[i], 1);
+        if (cluster > 1 && rank == 0) mbar_arrive_expect_tx(&loss_bar[i], 8 * cluster);
+      }
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&stat_bar[i], cluster > 1 ? 1 : kWarps);
+      if (cluster > 1) mbar_arrive_expect_tx(&stat_bar[i], 8 * kWarps * cluster);
       mbar_init(&next_full[i], 1);
       mbar_init(&next_free[i], cluster);
-      if (cluster > 1) mbar_arrive_expect_tx(&stat_bar[i], 16 * cluster);
-      if (kMode == ROW_DISTILL) {
-        mbar_init(&loss_bar[i], 1);
-        mbar_init(&result_full[i], 1);
-        mbar_init(&written[i], kWarps);
-        if (cluster > 1 && rank == 0) mbar_arrive_expect_tx(&loss_bar[i], 16 * cluster);
-      }
     }
     mbar_init_fence();
   }
@@ -527,54 +555,208 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
 
   if (stop) {
     // the whole cluster does nothing
+  } else if (wid < kWarps) {
+    // ---- statistics and gradients
+    int32_t b = 0;       // buffer of the next row with weight
+    uint32_t phase = 0;  // of the ring
+    uint32_t sent = 0;   // rows with weight so far
+    for (int32_t k = 0;; ++k) {
+      const int32_t slot = k % kJobs;
+      const uint32_t parity = (k / kJobs) & 1;
+      if (!wait_or_quit(&job_full[slot], parity, &quit)) break;
+      const RowJob& job = jobs[slot];
+      if (job.row < 0) break;
+      const Slice& sl = job.slice;
+      T* const dz = a.dlogits ? static_cast<T*>(a.dlogits) + job.row * a.dstride : nullptr;
+      if (!job.fetched) {  // a row that takes no part
+        if (dz) zero_slice<T, kThreads>(dz, sl, a.vocab);
+        __syncwarp();
+        if (lane == 0) {
+          if (kMode == ROW_DISTILL) mbar_arrive(&written[slot]);
+          mbar_arrive(&job_empty[slot]);
+        }
+        continue;
+      }
+      uint4* const buf = ring + b * shape.vecs;
+      uint64_t* const got = full + b * shape.chunks;
+      uint64_t* const freed = empty + b * shape.chunks;
+      const int32_t count = sl.count;
+      const int32_t mine = count - wid * 32 - lane;  // > u * kThreads: vector u of this thread exists
+
+      // The statistics: steps of a few vectors, their maximum first, so that
+      // the sum's shift changes rarely, and for the whole warp at once.
+      float m = -INFINITY, edge = -INFINITY;
+      Pair s = {0.0f, 0.0f};
+      if (sl.edge_count > 0 && wid == 0) {
+        if (lane < sl.edge_count)
+          edge = to_float(static_cast<const T*>(a.logits)[job.row * a.stride + edge_index(sl, lane, a.vocab)]);
+        m = warp_max_one(edge);
+        s.hi = exp_scaled(edge - softmax_shift(m), a.scale);
+      }
+      bool ok = true;
+      const uint4* from = buf + tid;
+      int32_t left = mine;
+      for (int j = 0; j < shape.chunks; ++j) {
+        if (!(ok = wait_or_quit(&got[j], phase, &quit))) break;
+#pragma unroll
+        for (int q = 0; q < kChunkSteps; ++q, from += kStep, left -= kStep) {
+          uint4 v[kVecsPerStep];
+          if (left + lane >= kStep) {  // the same for the warp
+#pragma unroll
+            for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
+          } else {
+            if (left + lane <= 0) continue;
+#pragma unroll
+            for (int u = 0; u < kVecsPerStep; ++u)
+              v[u] = left > u * kThreads ? from[u * kThreads] : make_uint4(kNone, kNone, kNone, kNone);
+          }
+          uint32_t packed = kNone;
+#pragma unroll
+          for (int u = 0; u < kVecsPerStep; ++u) packed = max_vector<T>(packed, v[u]);
+          const float top = warp_max_one(Word<T>::top(packed));
+          if (top > m) {
+            s = rescaled(m, s, top, a.scale);
+            m = top;
+          }
+          ExpSum sum(softmax_shift(m));
+#pragma unroll
+          for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], a.scale);
+          s.hi += sum.total();
+        }
+        if (kMode == ROW_SCORE) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&freed[j]);
+        }
+      }
+      if (!ok) break;
+      s.hi = warp_sum(s.hi);
+      s.lo = warp_sum(s.lo) + unbiased_sum(s.hi).lo;
+      // not before every block has read the row before the last
+      if (k > 0 && !wait_or_quit(&result_full[(k - 1) % kJobs], ((k - 1) / kJobs) & 1, &quit)) break;
+      const float2 own = make_float2(m, s.hi + s.lo);
+      if (cluster == 1) {
+        if (lane == 0) {
+          inbox[sent & 1][wid] = own;
+          mbar_arrive(&stat_bar[sent & 1]);
+        }
+      } else if (lane < cluster) {
+        cluster_send(&inbox[sent & 1][rank * kWarps + wid], &stat_bar[sent & 1], lane, own);
+      }
+      ++sent;
+
+      if (kMode != ROW_SCORE) {
+        // the gradient
+        if (!wait_or_quit(&result_full[slot], parity, &quit)) break;
+        const RowResult& r = results[slot];
+        if (r.stop) break;
+        T* const dv = dz + (sl.head + sl.first * N);
+        const Gradient grad(softmax_shift(r.st.m), r.g.k);
+        if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+          uint4* to = reinterpret_cast<uint4*>(dv) + tid;
+          from = buf + tid;
+          left = mine;
+          for (int j = 0; j < shape.chunks; ++j) {
+#pragma unroll
+            for (int q = 0; q < kChunkSteps; ++q, from += kStep, to += kStep, left -= kStep) {
+              if (left + lane >= kStep) {
+                uint4 v[kVecsPerStep];
+#pragma unroll
+                for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
+#pragma unroll
+                for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = grad.template of<T>(v[u], a.scale);
+              } else {
+#pragma unroll
+                for (int u = 0; u < kVecsPerStep; ++u)
+                  if (left > u * kThreads) to[u * kThreads] = grad.template of<T>(from[u * kThreads], a.scale);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&freed[j]);
+          }
+        } else {
+          // no gradient, zeros, or one laid out to another alignment than the logits
+          if (dz && r.idle) {
+            zero_slice<T, kThreads>(dz, sl, a.vocab);
+          } else if (dz) {
+            for (int32_t i = tid; i < count; i += kThreads) {
+              const uint4 d = grad.template of<T>(buf[i], a.scale);
+#pragma unroll
+              for (int e = 0; e < N; ++e) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + e, d, e);
+            }
+          }
+          __syncwarp();
+          if (lane == 0)
+            for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&freed[j]);
+        }
+        if (dz && !r.idle) {
+          if (kMode == ROW_POLICY && tid < sl.edge_count)
+            dz[edge_index(sl, tid, a.vocab)] = from_float<T>(grad.of(edge, a.scale));
+          // over the value just written, by the thread that wrote it
+          if (kMode == ROW_POLICY && tid == r.writer) dz[heads[slot].label] = from_float<T>(r.g.at_label);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (kMode == ROW_DISTILL) mbar_arrive(&written[slot]);
+        mbar_arrive(&job_empty[slot]);
+      }
+      if (++b == shape.buffers) {
+        b = 0;
+        phase ^= 1u;
+      }
+    }
   } else if (wid == kWarps) {
     // ---- the slices
     if (lane == 0) {
-      int32_t slot = 0, used = 0;  // the chunk to fill; chunks filled at least once
-      uint32_t phase = 0;          // of the ring
-      const int32_t slots = shape.buffers * shape.chunks;
+      int32_t chunk = 0, used = 0;  // the one to fill; those filled at least once
+      uint32_t phase = 0;           // of the ring
+      const int32_t chunks = shape.buffers * shape.chunks;
       bool ok = true;
       for (int32_t k = 0; ok; ++k) {
-        if (!(ok = wait_or_quit(&job_full[k & 1], (k >> 1) & 1, &quit))) break;
-        const RowJob job = jobs[k & 1];
-        mbar_arrive(&job_empty[k & 1]);
+        if (!(ok = wait_or_quit(&job_full[k % kJobs], (k / kJobs) & 1, &quit))) break;
+        const RowJob job = jobs[k % kJobs];
+        mbar_arrive(&job_empty[k % kJobs]);
         if (job.row < 0) break;
         if (!job.fetched) continue;
         const T* z = static_cast<const T*>(a.logits) + job.row * a.stride;
         const uint4* from = reinterpret_cast<const uint4*>(z + job.slice.head) + job.slice.first;
-        uint4* to = ring + slot / shape.chunks * shape.vecs;
+        uint4* to = ring + chunk / shape.chunks * shape.vecs;
         for (int32_t left = job.slice.count, j = 0; j < shape.chunks; ++j, left -= kChunk, from += kChunk, to += kChunk) {
-          if (!(ok = wait_or_quit(&empty[slot], phase ^ 1u, &quit))) break;
+          if (!(ok = wait_or_quit(&empty[chunk], phase ^ 1u, &quit))) break;
           const int32_t bytes = min(kChunk, max(0, left)) * 16;
-          mbar_arrive_expect_tx(&full[slot], bytes);
-          if (bytes > 0) bulk_load(to, from, bytes, &full[slot]);
-          used = max(used, ++slot);
-          if (slot == slots) {
-            slot = 0;
+          mbar_arrive_expect_tx(&full[chunk], bytes);
+          if (bytes > 0) bulk_load(to, from, bytes, &full[chunk]);
+          used = max(used, ++chunk);
+          if (chunk == chunks) {
+            chunk = 0;
             phase ^= 1u;
           }
         }
       }
       // Every copy has to land before the block ends, whether its row is still
       // wanted or not: chunk i was last filled in this pass over the ring if
-      // it lies before `slot`, else in the one before.
-      for (int32_t i = 0; i < used; ++i) mbar_wait(&full[i], i < slot ? phase : phase ^ 1u);
+      // it lies before `chunk`, else in the one before.
+      for (int32_t i = 0; i < used; ++i) mbar_wait(&full[i], i < chunk ? phase : phase ^ 1u);
     }
   } else if (wid == kWarps + 1) {
-    // ---- which rows, their scalars and teacher entries
-    int32_t row = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(cluster));
+    // ---- which rows, their scalars and teacher entries: a group of rows at a
+    // time, a lane each, so that the loads that depend on one another (weight,
+    // label, the label's logit) are waited for once a group
+    int32_t group = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(cluster));
+    int32_t k = 0;
     bool ok = true;
-    int32_t b = 0;        // ROW_DISTILL: buffer of the row before
-    uint32_t active = 0;  // and rows with entries so far
-    for (int32_t k = 0; ok; ++k) {
+    for (int32_t n = 0; ok; ++n) {
+      const int i = n & 1;
+      const int32_t first = group * shape.group;
+      const int32_t rows = group < 0 ? 1 : min(shape.group, a.rows - first);  // at the end one job that says so
+      const int32_t row = group < 0 ? -1 : first + min(lane, rows - 1);
       float weight = 0.0f;
-      if (row >= 0) {
-        // ask for row k + 1: its slot is free once every block has read row k - 1 from it
-        const int i = (k + 1) & 1;
+      if (group >= 0) {
+        // ask for the next group: the answer's place is free once every block has read the one before the last
         if (lane == 0) {
           mbar_arrive_expect_tx(&next_full[i], 16);
           if (rank == 0) {
-            ok = wait_or_quit(&next_free[i], ((k >> 1) & 1) ^ 1, &quit);
+            ok = wait_or_quit(&next_free[i], ((n >> 1) & 1) ^ 1, &quit);
             if (ok) request_row(&next[i], &next_full[i], cluster > 1);
           }
         }
@@ -582,294 +764,144 @@ __global__ void __launch_bounds__(kWarps * 32 + 64, kWarps == 8 ? 3 : 5)
         if (kMode == ROW_SCORE) weight = (!a.mask || a.mask[row]) ? 1.0f : 0.0f;
         else weight = a.weights[row];
       }
-      if (!ok || !(ok = wait_or_quit(&job_empty[k & 1], ((k >> 1) & 1) ^ 1, &quit))) break;
-      if (lane == 0) {
-        RowJob job;
-        job.row = row;
-        job.fetched = weight != 0.0f;
-        job.slice = row_slice(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, cluster);
-        jobs[k & 1] = job;
-        mbar_arrive(&job_full[k & 1]);
-      }
-      if (weight != 0.0f) {
-        RowHead h;
-        if (lane == 0) h = row_head<T, kMode>(a, row);
-        if (kMode == ROW_DISTILL) {
-          const Teacher te = teacher_at(teachers + (k & 1) * teacher_bytes(a.teacher_count), a.teacher_count);
-          h.mass = load_teacher(a, row, te, rank == 0);
+      RowJob job;
+      job.row = row;
+      job.fetched = weight != 0.0f;
+      job.slice = row_slice(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, cluster);
+      RowHead h = {};
+      for (int32_t j = 0; ok && j < rows; ++j, ++k) {
+        const int32_t slot = k % kJobs;
+        if (!(ok = wait_or_quit(&job_empty[slot], ((k / kJobs) & 1) ^ 1, &quit))) break;
+        if (lane == j) {
+          jobs[slot] = job;
+          mbar_arrive(&job_full[slot]);
         }
-        if (lane == 0) heads[k & 1] = h;
-      }
-      __syncwarp();
-      if (row >= 0 && lane == 0) mbar_arrive(&head_full[k & 1]);
-      if (kMode == ROW_DISTILL && k > 0 && jobs[(k - 1) & 1].fetched) {
-        // ---- meanwhile the row before has its statistics: its entries
-        const int32_t before = (k - 1) & 1;
-        if (!(ok = wait_or_quit(&result_full[active & 1], (active >> 1) & 1, &quit))) break;
-        const RowResult r = results[before];
-        const RowHead& h = heads[before];
-        const Slice& sl = jobs[before].slice;
-        const int64_t t = jobs[before].row;
-        if (r.stop) break;
-        const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
-        const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + sl.count * N;  // the slice's elements
-        const auto mine = [&](int32_t id) {
-          return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
-                 (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
-        };
-        const Teacher te = teacher_at(teachers + before * teacher_bytes(a.teacher_count), a.teacher_count);
-        const T* held = reinterpret_cast<const T*>(ring + b * shape.vecs);
-        const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
-        const float part = warp_sum(teacher_entries(a, te, h, r.st, lane, 32, mine, logit));
+        if (group < 0) break;
+        if (j == 0 && lane < rows && weight != 0.0f) h = row_head<T, kMode>(a, row);
         __syncwarp();
-        if (lane == 0)
-          for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&empty[b * shape.chunks + j]);
-        if (++b == shape.buffers) b = 0;
-        const uint32_t box = active & 1;
-        if (cluster > 1 && lane == 0)
-          cluster_send(&loss_box[box][rank], &loss_bar[box], 0, make_float4(part, 0.0f, 0.0f, 0.0f));
-        if (a.dlogits) {  // over the block's own values of the row
-          if (!(ok = wait_or_quit(&written[active & 1], (active >> 1) & 1, &quit))) break;
-          write_entries(a, te, static_cast<T*>(a.dlogits) + t * a.dstride, lane, 32, mine);
+        if (kMode == ROW_DISTILL && __shfl_sync(kFullMask, job.fetched, j)) {
+          const Teacher te = teacher_at(teachers + slot * teacher_bytes(a.teacher_count), a.teacher_count);
+          const float mass = load_teacher(a, first + j, te, rank == 0);
+          if (lane == j) h.mass = mass;
         }
-        if (rank == 0 && lane == 0) {
-          float loss = part;
-          if (cluster > 1) {
-            if (!cluster_receive(&loss_bar[box], (active >> 1) & 1)) status_set(a.status, THD_ERR_TIMEOUT);
-            loss = 0.0f;
-            for (int c = 0; c < cluster; ++c) loss += loss_box[box][c].x;
-            mbar_arrive_expect_tx(&loss_bar[box], 16 * cluster);
-          }
-          a.token_losses[t] = loss * (a.scale.tau * a.scale.tau);
-        }
-        ++active;
         __syncwarp();
+        if (lane == j) {
+          heads[slot] = h;
+          mbar_arrive(&head_full[slot]);
+        }
       }
-      if (row < 0) break;
+      if (!ok || group < 0) break;
       // the answer, which every block of the cluster gets
-      const int i = (k + 1) & 1;
-      if (!(ok = cluster_receive(&next_full[i], (k >> 1) & 1))) {
+      if (!(ok = cluster_receive(&next_full[i], (n >> 1) & 1))) {
         quit = 1;
         break;
       }
       const int32_t block = requested_block(&next[i]);
-      row = block < 0 ? -1 : static_cast<int32_t>(static_cast<uint32_t>(block) / static_cast<uint32_t>(cluster));
+      group = block < 0 ? -1 : static_cast<int32_t>(static_cast<uint32_t>(block) / static_cast<uint32_t>(cluster));
       __syncwarp();
       if (lane == 0) cluster_arrive0(&next_free[i]);
     }
   } else {
-  // ---- the rows
-  int32_t b = 0, k = 0;
-  uint32_t phase = 0, active = 0;  // active: rows exchanged with the cluster
-  for (;; ++k) {
-    // a warp that finds the job there after another gave up waiting for it
-    // gives up too: all of them meet at the barriers below
-    bool ok = wait_or_quit(&job_full[k & 1], (k >> 1) & 1, &quit) && !quit;
-    // read where they are needed: registers are for the sweeps
-    const RowHead& h = heads[k & 1];
-    const Slice& sl = jobs[k & 1].slice;
-    const int64_t t = jobs[k & 1].row;
-    if (ok && t < 0) break;
-    const uint4* const buf = ring + b * shape.vecs;
-    uint64_t* const got = full + b * shape.chunks;
-    uint64_t* const freed = empty + b * shape.chunks;
-
-    if (ok && !jobs[k & 1].fetched) {  // a row that takes no part
-      if (tid == 0 && rank == 0) write_idle_row<kMode>(a, t);
-      if (a.dlogits) zero_slice<T, kThreads>(static_cast<T*>(a.dlogits) + t * a.dstride, sl, a.vocab);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&job_empty[k & 1]);
-      continue;
-    }
-
-    const int32_t count = ok ? sl.count : 0;
-    float edge = -INFINITY;
-    if (ok && tid < sl.edge_count)
-      edge = to_float(static_cast<const T*>(a.logits)[t * a.stride + edge_index(sl, tid, a.vocab)]);
-    // the slice's maximum, chunk by chunk as they land
-    uint32_t packed = kNone;
-    {
-      const uint4* from = buf + tid;
-      int32_t left = count - wid * 32;  // vectors from the warp's first one on
-      for (int j = 0; ok && j < shape.chunks; ++j, from += kChunk, left -= kChunk) {
-        ok = wait_or_quit(&got[j], phase, &quit);
-        if (left >= kChunk) {
-#pragma unroll
-          for (int u = 0; u < kVecsPerStep; ++u) packed = max_vector<T>(packed, from[u * kThreads]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kVecsPerStep; ++u)
-            if (lane < left - u * kThreads) packed = max_vector<T>(packed, from[u * kThreads]);
-        }
-      }
-    }
-    const float top = warp_max_one(fmaxf(Word<T>::top(packed), edge));
-    if (lane == 0) maxima[wid] = ok ? top : NAN;  // NaN: this warp gave up
-    group_sync<kThreads>();
-    float m = maxima[0];
-    ok = m == m;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      ok &= maxima[w] == maxima[w];
-      m = fmaxf(m, maxima[w]);
-    }
-
-    if (!ok) {  // in every warp: a wait ran out, or the block was told to quit
-      if (wid == 0) {
-        if (cluster > 1 && lane < cluster)
-          cluster_send(&inbox[active & 1u][rank], &stat_bar[active & 1u], lane, make_float4(0.0f, 0.0f, 0.0f, 1.0f));
+    // ---- finishing rows
+    int32_t b = 0;
+    uint32_t got = 0;  // rows with weight so far
+    for (int32_t k = 0;; ++k) {
+      const int32_t slot = k % kJobs;
+      if (!wait_or_quit(&job_full[slot], (k / kJobs) & 1, &quit)) break;
+      const int64_t t = jobs[slot].row;
+      if (t < 0) break;
+      if (!jobs[slot].fetched) {
         if (lane == 0) {
-          status_set(a.status, THD_ERR_TIMEOUT);
-          quit = 1;
+          if (rank == 0) write_idle_row<kMode>(a, t);
+          mbar_arrive(&result_full[slot]);
+          mbar_arrive(&job_empty[slot]);
         }
+        continue;
       }
-      break;
-    }
-
-    // its sum of exponentials
-    {
-      ExpSum sum(softmax_shift(m));
-      const uint4* from = buf + tid;
-      int32_t left = count - wid * 32;
-      for (int j = 0; j < shape.chunks; ++j, from += kChunk, left -= kChunk) {
-        if (left >= kChunk) {
-          uint4 v[kVecsPerStep];
-#pragma unroll
-          for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
-#pragma unroll
-          for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], a.scale);
-        } else {
-#pragma unroll 1
-          for (int u = 0; u * kThreads < left; ++u)
-            sum.template add<T>(
-                lane < left - u * kThreads ? from[u * kThreads] : make_uint4(kNone, kNone, kNone, kNone), a.scale);
-        }
-        if (kMode == ROW_SCORE) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&freed[j]);
-        }
-      }
-      float part = sum.total();
-      if (tid < sl.edge_count) part += exp_scaled(edge - softmax_shift(m), a.scale);
-      part = warp_sum(part);
-      if (lane == 0) parts[active & 1u][wid] = part;
-    }
-    group_sync<kThreads>();
-    if (wid == 0) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += parts[active & 1u][w];
-      SoftmaxStat st = {m, unbiased_sum(s)};
-      bool off = !wait_or_quit(&head_full[k & 1], (k >> 1) & 1, &quit);
-      if (cluster > 1) {
-        const uint32_t box = active & 1u;
-        __syncwarp();
-        if (lane < cluster)
-          cluster_send(&inbox[box][rank], &stat_bar[box], lane, make_float4(st.m, st.s.hi, st.s.lo, off ? 1.0f : 0.0f));
-        off |= !cluster_receive(&stat_bar[box], (active >> 1) & 1u);
-        // one block's statistics a lane
-        const float4 in = lane < cluster ? inbox[box][lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-        off = __any_sync(kFullMask, off || in.w != 0.0f);
-        st.m = warp_max_one(in.x);
-        Pair s = rescaled(in.x, {in.y, in.z}, st.m, a.scale);
-#pragma unroll
-        for (int o = kMaxCluster / 2; o > 0; o >>= 1)
-          s = add(s, {__shfl_xor_sync(kFullMask, s.hi, o), __shfl_xor_sync(kFullMask, s.lo, o)});
-        st.s = {__shfl_sync(kFullMask, s.hi, 0), __shfl_sync(kFullMask, s.lo, 0)};
-        if (lane == 0) mbar_arrive_expect_tx(&stat_bar[box], 16 * cluster);  // for the row after the next
-      }
+      const uint32_t box = got & 1;
       RowResult r;
-      r.st = st;
-      r.g = {0.0f, 0.0f};
-      r.stop = off;
-      r.idle = !off && h.weight == 0.0f;  // a label out of range
-      if (r.idle) {
-        if (lane == 0 && rank == 0) write_idle_row<kMode>(a, t);
-      } else if (!off) {
-        r.g = finish_row<kMode>(a, t, h, st, lane == 0 && rank == 0);
-      }
-      if (lane == 0) {
-        results[k & 1] = r;
-        if (kMode == ROW_DISTILL) mbar_arrive(&result_full[active & 1u]);
-        if (off) {
-          status_set(a.status, THD_ERR_TIMEOUT);
-          quit = 1;
-        }
-      }
-    }
-
-    if (kMode != ROW_SCORE) {
-      group_sync<kThreads>();
-      const RowResult r = results[k & 1];
-      if (r.stop) break;  // no block of the cluster writes any more
-      const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + count * N;  // the slice's elements
-      const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
-      T* const dz = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
+      r.stop = !wait_or_quit(&head_full[slot], (k / kJobs) & 1, &quit) ||
+               !cluster_receive(&stat_bar[box], (got >> 1) & 1);
+      // up to two warps' statistics a lane
+      const int32_t n = cluster * kWarps;
+      const float2 none = make_float2(-INFINITY, 0.0f);
+      const float2 in0 = lane < n ? inbox[box][lane] : none, in1 = lane + 32 < n ? inbox[box][lane + 32] : none;
+      r.st.m = warp_max_one(fmaxf(in0.x, in1.x));
+      const Pair s0 = rescaled(in0.x, {in0.y, 0.0f}, r.st.m, a.scale);
+      const Pair s1 = rescaled(in1.x, {in1.y, 0.0f}, r.st.m, a.scale);
+      r.st.s = {warp_sum(s0.hi + s1.hi), warp_sum(s0.lo + s1.lo)};
+      const RowHead& h = heads[slot];
+      const Slice& sl = jobs[slot].slice;
+      const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + sl.count * N;  // the slice's elements
       const auto mine = [&](int32_t id) {
         return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
                (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
       };
-      const Gradient grad(softmax_shift(r.st.m), r.g.k);
-      T* const dv = dz + lo_v;
-      if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
-        const uint4* from = buf + tid;
-        uint4* to = reinterpret_cast<uint4*>(dv) + tid;
-        int32_t left = count - wid * 32;
-        for (int j = 0; j < shape.chunks; ++j, from += kChunk, to += kChunk, left -= kChunk) {
-          if (left >= kChunk) {
-            uint4 v[kVecsPerStep];
-#pragma unroll
-            for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
-#pragma unroll
-            for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = grad.template of<T>(v[u], a.scale);
-          } else {
-#pragma unroll 1
-            for (int u = 0; u * kThreads < left; ++u)
-              if (lane < left - u * kThreads) to[u * kThreads] = grad.template of<T>(from[u * kThreads], a.scale);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&freed[j]);
-        }
-      } else {
-        // no gradient, zeros, or one laid out to another alignment than the logits
-        if (dz && r.idle) {
-          zero_slice<T, kThreads>(dz, sl, a.vocab);
-        } else if (dz) {
-          for (int32_t i = tid; i < count; i += kThreads) {
-            const uint4 d = grad.template of<T>(buf[i], a.scale);
-#pragma unroll
-            for (int e = 0; e < N; ++e) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + e, d, e);
-          }
-        }
-        __syncwarp();
-        if (lane == 0)
-          for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&freed[j]);
-      }
-      if (dz && !r.idle) {
-        if (tid < sl.edge_count) dz[edge_index(sl, tid, a.vocab)] = from_float<T>(grad.of(edge, a.scale));
+      r.g = {0.0f, 0.0f};
+      r.writer = -1;
+      r.idle = !r.stop && h.weight == 0.0f;  // a label out of range
+      if (r.idle) {
+        if (lane == 0 && rank == 0) write_idle_row<kMode>(a, t);
+      } else if (!r.stop) {
+        r.g = finish_row<kMode>(a, t, h, r.st, lane == 0 && rank == 0);
         if (kMode == ROW_POLICY && mine(h.label)) {
-          // over the value just written, by the thread that wrote it
-          const int32_t in = h.label - lo_v;
-          int32_t writer = in / N % kThreads;
-          if (in < 0) writer = h.label;                                            // the head
-          else if (h.label >= hi_v) writer = sl.edge_count - (a.vocab - h.label);  // the tail
-          if (tid == writer) dz[h.label] = from_float<T>(r.g.at_label);
+          const int32_t in_slice = h.label - lo_v;
+          r.writer = in_slice / N % kThreads;
+          if (in_slice < 0) r.writer = h.label;                                            // the head
+          else if (h.label >= hi_v) r.writer = sl.edge_count - (a.vocab - h.label);  // the tail
         }
       }
-      if (kMode == ROW_DISTILL) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&written[active & 1u]);
+      __syncwarp();
+      if (lane == 0) {
+        results[slot] = r;
+        if (cluster > 1) mbar_arrive_expect_tx(&stat_bar[box], 8 * kWarps * cluster);  // for the row after the next
+        mbar_arrive(&result_full[slot]);
+        if (r.stop) quit = 1;
       }
-    }
-    ++active;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&job_empty[k & 1]);
-    if (++b == shape.buffers) {
-      b = 0;
-      phase ^= 1u;
+      if (r.stop) break;
+      if (kMode == ROW_DISTILL) {
+        const Teacher te = teacher_at(teachers + slot * teacher_bytes(a.teacher_count), a.teacher_count);
+        const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
+        const T* const held = reinterpret_cast<const T*>(ring + b * shape.vecs);
+        const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
+        const float part = warp_sum(teacher_entries(a, te, h, r.st, lane, 32, mine, logit));
+        __syncwarp();
+        if (lane == 0) {
+          for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&empty[b * shape.chunks + j]);
+          if (cluster > 1)
+            cluster_send(&loss_box[got % kJobs][rank], &loss_bar[got % kJobs], 0, make_float2(part, 0.0f));
+        }
+        if (++b == shape.buffers) b = 0;
+        if (a.dlogits) {
+          T* const dz = static_cast<T*>(a.dlogits) + t * a.dstride;
+          // the edges' logits have been read above, whichever matrix they are in
+          if (lane < sl.edge_count) {
+            const int32_t e = edge_index(sl, lane, a.vocab);
+            const Gradient grad(softmax_shift(r.st.m), r.g.k);
+            dz[e] = from_float<T>(grad.of(to_float(z[e]), a.scale));
+          }
+          // the entries over the block's own values of the row
+          if (!wait_or_quit(&written[slot], (k / kJobs) & 1, &quit)) break;
+          __syncwarp();
+          write_entries(a, te, dz, lane, 32, mine);
+        }
+        if (rank == 0 && lane == 0) {
+          float loss = part;
+          if (cluster > 1) {
+            if (!cluster_receive(&loss_bar[got % kJobs], (got / kJobs) & 1)) quit = 1;
+            loss = 0.0f;
+            for (int c = 0; c < cluster; ++c) loss += loss_box[got % kJobs][c].x;
+            mbar_arrive_expect_tx(&loss_bar[got % kJobs], 8 * cluster);
+          }
+          a.token_losses[t] = loss * (a.scale.tau * a.scale.tau);
+        }
+      }
+      ++got;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&job_empty[slot]);
     }
   }
-  }
+  if (lane == 0 && quit) status_set(a.status, THD_ERR_TIMEOUT);
   // no block ends while another may still send to it
   if (cluster > 1) cluster_sync();
 }
@@ -929,6 +961,7 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
     RowResult r;
     r.st = st;
     r.g = finish_row<kMode>(a, t, h, st, lane == 0);
+    r.writer = -1;
     r.stop = r.idle = false;
     if (lane == 0) result = r;
   }
@@ -963,24 +996,22 @@ thd_status_t done(cudaError_t e) {
 
 // Shared memory of an SM and what a block takes of it besides its buffers.
 constexpr int64_t kSmShared = 228 * 1024;
-constexpr int64_t kBlockShared = 1024 + 832;  // the driver's 1 KiB and the static arrays
-// Three blocks share an SM, each in a phase of its own: one waits for its
-// logits or its cluster while another computes or writes.
-constexpr int64_t kBlockBudget = kSmShared / 3 - kBlockShared;
+constexpr int64_t kBlockShared = 1024 + 2560;  // the driver's 1 KiB and the static arrays
+constexpr int64_t kBlockBudget = kSmShared / EXP_PER - kBlockShared;
 // Below this a slice is not divided further for want of rows.
 constexpr int64_t kSmallestSlice = 8 * 1024;
 
 template <typename T, int kMode, int kWarps>
 cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaStream_t s) {
   auto* kernel = row_cluster_kernel<T, kMode, kWarps>;
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {  // 48 KiB, the static arrays among them, need no leave
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   const int32_t cluster = shape.cluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kWarps * 32 + 64);
+  cfg.blockDim = dim3(kWarps * 32 + 96);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -992,7 +1023,7 @@ cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaS
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + shape.group - 1) / shape.group) * cluster);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, shape);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
@@ -1000,25 +1031,28 @@ cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaS
 template <typename T, int kMode>
 thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
-  const int64_t entries = kMode == ROW_DISTILL ? 2 * static_cast<int64_t>(teacher_bytes(a.teacher_count)) : 0;
+  const int64_t entries = kMode == ROW_DISTILL ? kJobs * static_cast<int64_t>(teacher_bytes(a.teacher_count)) : 0;
   const int sms = sm_count();
   // vectors of a block's slice when `cluster` blocks share the row
   const auto slice_of = [&](int32_t cluster) { return ((row + 15) / 16 + cluster - 1) / cluster; };
   RingShape shape;
   shape.cluster = 1;
-  while (shape.cluster < kMaxCluster && slice_of(shape.cluster) * 16 + entries > kBlockBudget) ++shape.cluster;
+  while (shape.cluster < kMaxCluster && EXP_ROWS * slice_of(shape.cluster) * 16 + entries > kBlockBudget) ++shape.cluster;
   while (shape.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * (shape.cluster + 1) <= sms &&
          slice_of(shape.cluster + 1) * 16 >= kSmallestSlice)
     ++shape.cluster;
   const int64_t slice = slice_of(shape.cluster);
+  shape.group = EXP_G;
+  while (shape.group > 1 && static_cast<int64_t>(a.rows) * shape.cluster < 16ll * sms * shape.group) shape.group /= 2;
   if (slice * 16 + entries > kMaxSlice || static_cast<int64_t>(a.rows) * shape.cluster > INT32_MAX)
     return done(launch_pdl(row_plain_kernel<T, kMode>, dim3(static_cast<unsigned>(a.rows)), dim3(kPlainThreads),
-                           static_cast<size_t>(entries / 2), s, a));
+                           static_cast<size_t>(entries / kJobs), s, a));
   const int warps = slice <= 512 ? 4 : 8;
-  const int64_t step = warps * 32 * kVecsPerStep;
+  const int64_t step = warps * 32 * kVecsPerStep * kChunkSteps;
   shape.vecs = static_cast<int32_t>(slice);
   shape.chunks = static_cast<int32_t>(std::max<int64_t>(1, (slice + step - 1) / step));
-  const int64_t fit = (kBlockBudget / (warps == 4 ? 4 : 1) - entries) / std::max<int64_t>(16, slice * 16);
+  const int64_t room = slice * 16 + entries <= kBlockBudget ? kBlockBudget : kMaxSlice;
+  const int64_t fit = ((warps == 4 ? kBlockBudget / 2 : room) - entries) / std::max<int64_t>(16, slice * 16);
   shape.buffers = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fit, kMaxChunks / shape.chunks)));
   const size_t smem = static_cast<size_t>(shape.buffers * slice * 16 + entries);
   if (warps == 4) return done(launch_cluster<T, kMode, 4>(a, shape, smem, s));
