@@ -14,15 +14,14 @@
 namespace thd {
 
 // What a logit is multiplied by: inv_tau, the reciprocal of the temperature in
-// 32 bits, and in the kernels' exponents log2(e) * inv_tau as the sum of two
-// floats.  hi is rounded towards zero, so lo > 0 and d*hi + d*lo never mixes
-// infinities of both signs.  A softmax scaled by hi alone is that of a
-// temperature up to 6e-8 off: the same error in every row, which sums of
-// log-probabilities over a document add up.
+// 32 bits, and in the kernels' exponents log2(e) * inv_tau = hi + lo with hi
+// rounded to 32 bits.  A softmax scaled by hi alone is that of a temperature
+// up to 6e-8 off: the same error in every row, which sums of log-probabilities
+// over a document add up.
 struct LogitScale {
   float hi, lo;
   float tau, inv_tau;
-  uint64_t hi2, lo2;  // {hi, hi} and {lo, lo} for the packed instructions
+  uint64_t hi2;  // {hi, hi} for the packed instructions
 };
 
 inline LogitScale make_logit_scale(float temperature) {
@@ -31,13 +30,10 @@ inline LogitScale make_logit_scale(float temperature) {
   s.inv_tau = 1.0f / temperature;
   const double c = 1.4426950408889634 * static_cast<double>(s.inv_tau);
   s.hi = static_cast<float>(c);
-  if (static_cast<double>(s.hi) >= c) s.hi = std::nextafterf(s.hi, 0.0f);
   s.lo = static_cast<float>(c - static_cast<double>(s.hi));
   uint32_t bits;
   std::memcpy(&bits, &s.hi, 4);
   s.hi2 = uint64_t(bits) << 32 | bits;
-  std::memcpy(&bits, &s.lo, 4);
-  s.lo2 = uint64_t(bits) << 32 | bits;
   return s;
 }
 
@@ -47,8 +43,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 2^(d * log2(e) * inv_tau) = exp(d * inv_tau)
-__device__ __forceinline__ float exp_scaled(float d, const LogitScale& c) { return ex2(fmaf(d, c.hi, d * c.lo)); }
+// exp(d * inv_tau).  An infinite d stays one: lo is only added to what is finite.
+__device__ __forceinline__ float exp_scaled(float d, const LogitScale& c) {
+  const float x = d * c.hi;
+  return ex2(fabsf(x) < INFINITY ? fmaf(d, c.lo, x) : x);
+}
 
 // ---------------------------------------------------------------------------
 // element types
@@ -130,30 +129,47 @@ __device__ __forceinline__ Pair log2_pair(Pair sum) {
 // of log-probabilities over a document would add it up.
 constexpr float kEx2Bias = 5.1e-8f;
 
-// Running maximum m of some logits and the sum s of exp((z - shift(m)) / tau).
-// The shift is m itself, or 0 while m is not finite: a set whose logits are
-// all -inf then has s = 0, one that holds +inf has s = +inf, and a NaN makes
-// s NaN, without a case of its own.
+// Running maximum m of some logits and the sum s of their exponentials
+// relative to it, in one of three ways (a fourth needs no case of its own: a
+// NaN makes s NaN):
+//   m * hi is finite: s sums 2^(z hi - x), x = m * hi rounded, so that an
+//     exponent is one fused multiply-add; row_norm() makes up for the rounding
+//   m is finite, m * hi is not ("far": logits at a type's lowest value):
+//     s sums 2^((z - m) hi)
+//   m is not finite: s sums 2^(z hi), so it is 0 where no logit is above -inf
+//     and +inf where one is +inf
 struct SoftmaxStat {
   float m;
   Pair s;
 };
 
-__device__ __forceinline__ float softmax_shift(float m) { return fabsf(m) < INFINITY ? m : 0.0f; }
+__device__ __forceinline__ float softmax_shift(float m, const LogitScale& c) {
+  const float x = m * c.hi;
+  return fabsf(x) < INFINITY ? x : 0.0f;
+}
+__device__ __forceinline__ bool softmax_far(float m, const LogitScale& c) {
+  return fabsf(m) < INFINITY && !(fabsf(m * c.hi) < INFINITY);
+}
+// one term of the sum
+__device__ __forceinline__ float softmax_term(float z, float m, const LogitScale& c) {
+  return softmax_far(m, c) ? ex2((z - m) * c.hi) : ex2(fmaf(z, c.hi, -softmax_shift(m, c)));
+}
 
-__device__ __forceinline__ SoftmaxStat empty_stat() { return {-INFINITY, {0.0f, 0.0f}}; }
-
-// The sum of a set with maximum m, rescaled to the shift of the larger maximum
-// `to`.  One factor scales a whole partial sum, so the rounding of its
-// exponent and the mean error of ex2 go into the low part.
+// The sum of a set with maximum m, rescaled to the larger maximum `to`.  One
+// factor scales a whole partial sum, so what its exponent lacks and the mean
+// error of ex2 go into the low part.
 __device__ __forceinline__ Pair rescaled(float m, Pair s, float to, const LogitScale& c) {
   if (m == to || s.hi == 0.0f) return s;
-  const float d = softmax_shift(m) - softmax_shift(to);
-  const float x = d * c.hi;
-  const float f = ex2(x);
-  const float rest = fmaf(d, c.hi, -x) + d * c.lo;
+  Pair d;
+  if (softmax_far(m, c) || softmax_far(to, c)) {
+    d = {fabsf(to) < INFINITY ? (m - to) * c.hi : m * c.hi, 0.0f};
+  } else {
+    d = two_sum(softmax_shift(m, c), -softmax_shift(to, c));
+    if (fabsf(to) < INFINITY && fabsf(m) < INFINITY) d.lo = fmaf(m - to, c.lo, d.lo);
+  }
+  const float f = ex2(d.hi);
   const float hi = s.hi * f;
-  const float lo = fmaf(s.hi, f, -hi) + hi * fmaf(rest, 0.693147181f, kEx2Bias) + s.lo * f;
+  const float lo = fmaf(s.hi, f, -hi) + hi * fmaf(d.lo, 0.693147181f, kEx2Bias) + s.lo * f;
   return {hi, f > 0.0f && fabsf(hi) < INFINITY ? lo : 0.0f};
 }
 
@@ -165,24 +181,28 @@ __device__ __forceinline__ Pair unbiased_sum(float s) {
 // A row none of whose logits is above -inf: its probabilities are taken as 0.
 __device__ __forceinline__ bool stat_is_empty(SoftmaxStat t) { return t.m == -INFINITY && t.s.hi == 0.0f; }
 
-// A row's log of its sum (relative to the shift), kept for its scalars.
+// A row's log of its sum, kept for its scalars: lse = base * inv_tau + log_sum.
 struct RowNorm {
-  float shift;  // softmax_shift(m)
+  float base;  // the maximum, 0 where that is not finite
   Pair log_sum;
 };
 
-__device__ __forceinline__ RowNorm row_norm(SoftmaxStat t) {
-  return {softmax_shift(t.m), scaled(log2_pair(t.s), kLn2Hi, kLn2Lo)};
+__device__ __forceinline__ RowNorm row_norm(SoftmaxStat t, const LogitScale& c) {
+  Pair l = log2_pair(t.s);
+  const float x = t.m * c.hi;
+  // the sum is relative to the rounded product: take back what rounding added
+  if (fabsf(x) < INFINITY) l = add(l, {-fmaf(t.m, c.hi, -x), 0.0f});
+  return {fabsf(t.m) < INFINITY ? t.m : 0.0f, scaled(l, kLn2Hi, kLn2Lo)};
 }
 
 // Logarithm of the probability of a logit z, as a pair.  Its error is that of
 // the sum: the large numbers z and m are subtracted before anything is rounded.
 __device__ __forceinline__ Pair log_prob(float z, const RowNorm& r, const LogitScale& c) {
-  return add(scaled(two_sum(z, -r.shift), c.inv_tau, 0.0f), {-r.log_sum.hi, -r.log_sum.lo});
+  return add(scaled(two_sum(z, -r.base), c.inv_tau, 0.0f), {-r.log_sum.hi, -r.log_sum.lo});
 }
 
 __device__ __forceinline__ float log_sum_exp(const RowNorm& r, const LogitScale& c) {
-  const Pair n = add(scaled({r.shift, 0.0f}, c.inv_tau, 0.0f), r.log_sum);
+  const Pair n = add(scaled({r.base, 0.0f}, c.inv_tau, 0.0f), r.log_sum);
   return n.hi + n.lo;
 }
 

@@ -43,7 +43,7 @@ struct RowArgs {
   int32_t teacher_dtype, teacher_count, normalize;
 };
 
-// dz_v = k * exp((z_v - shift) / tau), and `at_label` in the label's place
+// dz_v = k * the row's term of z_v (SoftmaxStat), and `at_label` in the label's place
 struct RowGrad {
   float k, at_label;
 };
@@ -107,7 +107,7 @@ __device__ __forceinline__ Pair label_logprob(float z, SoftmaxStat st, const Row
 }
 
 __device__ __forceinline__ void write_score(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st) {
-  const RowNorm r = row_norm(st);
+  const RowNorm r = row_norm(st, a.scale);
   const Pair lp = label_logprob(h.z_label, st, r, a.scale);
   a.logprobs[t] = lp.hi + lp.lo;
   a.lse[t] = log_sum_exp(r, a.scale);
@@ -119,7 +119,7 @@ __device__ __forceinline__ void write_score(const RowArgs& a, int64_t t, const R
 // and rounding it first would cost that difference about 5e-7.
 __device__ __forceinline__ RowGrad policy_row(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st,
                                               bool write) {
-  const RowNorm r = row_norm(st);
+  const RowNorm r = row_norm(st, a.scale);
   const Pair lp = label_logprob(h.z_label, st, r, a.scale);
   const float ratio = expf((lp.hi - h.old_lp) + lp.lo);
   // comparisons, not min/max: a NaN ratio stays one
@@ -206,7 +206,8 @@ __device__ __forceinline__ float load_teacher(const RowArgs& a, int64_t t, const
   if (bad && report) status_set(a.status, THD_ERR_INDEX_RANGE);
   float norm = 0.0f;
   if (a.normalize) {
-    top = softmax_shift(warp_max(top));
+    top = warp_max(top);
+    if (!(fabsf(top) < INFINITY)) top = 0.0f;
     float sum = 0.0f;
     for (int k = lane; k < K; k += 32) sum += exp_scaled(s.lq[k] - top, a.scale);
     sum = warp_sum(sum);

@@ -11,18 +11,6 @@
 
 #include "loss_internal.cuh"
 
-#ifndef EXP_MINB
-#define EXP_MINB 3
-#endif
-#ifndef EXP_G
-#define EXP_G 4
-#endif
-#ifndef EXP_ROWS
-#define EXP_ROWS 1
-#endif
-#ifndef EXP_PER
-#define EXP_PER 3
-#endif
 namespace thd {
 namespace {
 
@@ -180,17 +168,24 @@ __device__ __forceinline__ uint32_t max_vector(uint32_t m, const uint4& v) {
   return Word<T>::max2(Word<T>::max2(Word<T>::max2(m, v.x), Word<T>::max2(v.y, v.z)), v.w);
 }
 
-// Sums of exp((z - shift) * inv_tau) over vectors.
+// A thread's part of a SoftmaxStat's sum over vectors.
+//
+// Scaling by hi instead of hi + lo costs a term the factor 2^((z - m) lo), of
+// which the first order, 1 + ln2 (lo / hi) t for the exponent t, is enough.
+// `tilt` samples the sum of its second part: one element of each vector
+// stands for all of them, since the whole of it is below 1e-6 of the sum.
 struct ExpSum {
-  uint64_t neg, acc[2];
+  uint64_t acc[2] = {0, 0};
+  float tilt = 0.0f;
 
-  __device__ __forceinline__ explicit ExpSum(float shift) : neg(pack2(-shift, -shift)), acc{0, 0} {}
   template <typename T>
-  __device__ __forceinline__ void add(const uint4& v, const LogitScale& c) {
+  __device__ __forceinline__ void add(const uint4& v, uint64_t neg_shift, const LogitScale& c) {
 #pragma unroll
     for (int i = 0; i < Word<T>::kPairs; ++i) {
-      const uint64_t d = add2(Word<T>::pair(v, i), neg);
-      acc[i & 1] = add2(acc[i & 1], ex2_2(fma2(d, c.hi2, mul2(d, c.lo2))));
+      const uint64_t t = fma2(Word<T>::pair(v, i), c.hi2, neg_shift);
+      const uint64_t e = ex2_2(t);
+      if (i == 0) tilt = fmaf(unpack2(e).x, fmaxf(unpack2(t).x, -1e4f), tilt);
+      acc[i & 1] = add2(acc[i & 1], e);
     }
   }
   __device__ __forceinline__ float total() const {
@@ -199,21 +194,55 @@ struct ExpSum {
   }
 };
 
-// k * exp((z - shift) * inv_tau) of a vector, rounded to its type.
+template <typename T>
+__device__ __forceinline__ float tilt_correction(float tilt, const LogitScale& c) {
+  return tilt * (Word<T>::kElems * 0.693147181f * (c.lo / c.hi));
+}
+
+// The sum over a vector where the maximum is far; out of line, like all that
+// rows seldom take, so that what they always take stays in the instruction
+// cache of warps that are each somewhere else in it.
+template <typename T>
+__device__ __noinline__ float far_sum(uint4 v, float m, const LogitScale& c) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < Word<T>::kPairs; ++i) {
+    const float2 z = unpack2(Word<T>::pair(v, i));
+    s += ex2((z.x - m) * c.hi) + ex2((z.y - m) * c.hi);
+  }
+  return s;
+}
+
+// k * a row's terms, rounded to the logits' type.
 struct Gradient {
   uint64_t neg, k2;
+  float m;
 
-  __device__ __forceinline__ Gradient(float shift, float k) : neg(pack2(-shift, -shift)), k2(pack2(k, k)) {}
+  __device__ __forceinline__ Gradient(float m_, float k, const LogitScale& c) : k2(pack2(k, k)), m(m_) {
+    const float x = softmax_shift(m_, c);
+    neg = pack2(-x, -x);
+  }
   template <typename T>
   __device__ __forceinline__ uint4 of(const uint4& v, const LogitScale& c) const {
     uint4 d;
 #pragma unroll
     for (int j = 0; j < Word<T>::kPairs; ++j)
-      Word<T>::set_pair(d, j, mul2(k2, ex2_2(mul2(add2(Word<T>::pair(v, j), neg), c.hi2))));
+      Word<T>::set_pair(d, j, mul2(k2, ex2_2(fma2(Word<T>::pair(v, j), c.hi2, neg))));
     return d;
   }
   __device__ __forceinline__ float of(float z, const LogitScale& c) const {
-    return unpack2(k2).x * ex2((z + unpack2(neg).x) * c.hi);
+    return unpack2(k2).x * softmax_term(z, m, c);
+  }
+  // any maximum, element by element
+  template <typename T>
+  __device__ __forceinline__ uint4 of_any(const uint4& v, const LogitScale& c) const {
+    uint4 d;
+#pragma unroll
+    for (int j = 0; j < Word<T>::kPairs; ++j) {
+      const float2 z = unpack2(Word<T>::pair(v, j));
+      Word<T>::set_pair(d, j, pack2(of(z.x, c), of(z.y, c)));
+    }
+    return d;
   }
 };
 
@@ -244,7 +273,7 @@ struct RowResult {
 template <class Mine, class Logit>
 __device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher& te, const RowHead& h, SoftmaxStat st,
                                                  int32_t first, int32_t step, Mine mine, Logit logit) {
-  const RowNorm norm = row_norm(st);
+  const RowNorm norm = row_norm(st, a.scale);
   const float gs = a.grad_scale * h.weight * a.scale.tau;
   const bool empty = stat_is_empty(st);
   float loss = 0.0f;
@@ -427,8 +456,20 @@ __device__ __forceinline__ int32_t edge_index(const Slice& s, int32_t i, int32_t
   return i < s.head ? i : V - (s.edge_count - i);
 }
 
+// The gradient of a slice where it cannot be stored in vectors or the maximum
+// is far.
 template <typename T, int kThreads>
-__device__ __forceinline__ void zero_slice(T* dz, const Slice& sl, int32_t V) {
+__device__ __noinline__ void any_gradient(T* dv, const uint4* held, int32_t count, Gradient grad, const LogitScale& c) {
+  constexpr int N = Word<T>::kElems;
+  for (int32_t i = threadIdx.x; i < count; i += kThreads) {
+    const uint4 d = grad.of_any<T>(held[i], c);
+#pragma unroll
+    for (int e = 0; e < N; ++e) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + e, d, e);
+  }
+}
+
+template <typename T, int kThreads>
+__device__ __noinline__ void zero_slice(T* dz, const Slice& sl, int32_t V) {
   constexpr int N = Word<T>::kElems;
   T* dv = dz + sl.head + static_cast<int64_t>(sl.first) * N;
   if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
@@ -493,8 +534,8 @@ struct RowJob {
 // Statistics of row n (rows with weight counted) go to box n % 2.  A warp
 // sends row n when its block has the result of row n - 1, so every block has
 // sent row n - 1, and had the result of row n - 2: that box has been read.
-template <typename T, int kMode, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
+template <typename T, int kMode, int kWarps, int kPerSm>
+__global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
     row_cluster_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
   constexpr int N = Word<T>::kElems;
   constexpr int kThreads = kWarps * 32;
@@ -587,18 +628,21 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
       // the sum's shift changes rarely, and for the whole warp at once.
       float m = -INFINITY, edge = -INFINITY;
       Pair s = {0.0f, 0.0f};
+      float tilt = 0.0f;
+      uint64_t neg_shift = 0;
       if (sl.edge_count > 0 && wid == 0) {
         if (lane < sl.edge_count)
           edge = to_float(static_cast<const T*>(a.logits)[job.row * a.stride + edge_index(sl, lane, a.vocab)]);
         m = warp_max_one(edge);
-        s.hi = exp_scaled(edge - softmax_shift(m), a.scale);
+        neg_shift = pack2(-softmax_shift(m, a.scale), -softmax_shift(m, a.scale));
+        s.hi = softmax_term(edge, m, a.scale);
       }
       bool ok = true;
       const uint4* from = buf + tid;
       int32_t left = mine;
       for (int j = 0; j < shape.chunks; ++j) {
         if (!(ok = wait_or_quit(&got[j], phase, &quit))) break;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < kChunkSteps; ++q, from += kStep, left -= kStep) {
           uint4 v[kVecsPerStep];
           if (left + lane >= kStep) {  // the same for the warp
@@ -615,13 +659,29 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
           for (int u = 0; u < kVecsPerStep; ++u) packed = max_vector<T>(packed, v[u]);
           const float top = warp_max_one(Word<T>::top(packed));
           if (top > m) {
+            s.lo += tilt_correction<T>(tilt, a.scale);
+            tilt = 0.0f;
             s = rescaled(m, s, top, a.scale);
             m = top;
+            const float x = softmax_shift(m, a.scale);
+            neg_shift = pack2(-x, -x);
           }
-          ExpSum sum(softmax_shift(m));
+          if (softmax_far(m, a.scale)) {
 #pragma unroll
-          for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], a.scale);
+            for (int u = 0; u < kVecsPerStep; ++u) s.hi += far_sum<T>(v[u], m, a.scale);
+            continue;
+          }
+          ExpSum sum;
+          if (left + lane >= kStep) {
+#pragma unroll
+            for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], neg_shift, a.scale);
+          } else {  // as many as the warp has
+#pragma unroll
+            for (int u = 0; u < kVecsPerStep; ++u)
+              if (left + lane > u * kThreads) sum.template add<T>(v[u], neg_shift, a.scale);
+          }
           s.hi += sum.total();
+          tilt += sum.tilt;
         }
         if (kMode == ROW_SCORE) {
           __syncwarp();
@@ -629,8 +689,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
         }
       }
       if (!ok) break;
+      s.lo += tilt_correction<T>(tilt, a.scale);
       s.hi = warp_sum(s.hi);
       s.lo = warp_sum(s.lo) + unbiased_sum(s.hi).lo;
+      if (!(fabsf(s.hi) < INFINITY)) s.lo = 0.0f;
       // not before every block has read the row before the last
       if (k > 0 && !wait_or_quit(&result_full[(k - 1) % kJobs], ((k - 1) / kJobs) & 1, &quit)) break;
       const float2 own = make_float2(m, s.hi + s.lo);
@@ -650,16 +712,16 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
         const RowResult& r = results[slot];
         if (r.stop) break;
         T* const dv = dz + (sl.head + sl.first * N);
-        const Gradient grad(softmax_shift(r.st.m), r.g.k);
-        if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+        const Gradient grad(r.st.m, r.g.k, a.scale);
+        if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0 && !softmax_far(r.st.m, a.scale)) {
           uint4* to = reinterpret_cast<uint4*>(dv) + tid;
           from = buf + tid;
           left = mine;
           for (int j = 0; j < shape.chunks; ++j) {
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < kChunkSteps; ++q, from += kStep, to += kStep, left -= kStep) {
+              uint4 v[kVecsPerStep];
               if (left + lane >= kStep) {
-                uint4 v[kVecsPerStep];
 #pragma unroll
                 for (int u = 0; u < kVecsPerStep; ++u) v[u] = from[u * kThreads];
 #pragma unroll
@@ -674,16 +736,9 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
             if (lane == 0) mbar_arrive(&freed[j]);
           }
         } else {
-          // no gradient, zeros, or one laid out to another alignment than the logits
-          if (dz && r.idle) {
-            zero_slice<T, kThreads>(dz, sl, a.vocab);
-          } else if (dz) {
-            for (int32_t i = tid; i < count; i += kThreads) {
-              const uint4 d = grad.template of<T>(buf[i], a.scale);
-#pragma unroll
-              for (int e = 0; e < N; ++e) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + e, d, e);
-            }
-          }
+          // no gradient, zeros, one laid out to another alignment than the logits, or a far maximum
+          if (dz && r.idle) zero_slice<T, kThreads>(dz, sl, a.vocab);
+          else if (dz) any_gradient<T, kThreads>(dv, buf, count, grad, a.scale);
           __syncwarp();
           if (lane == 0)
             for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&freed[j]);
@@ -877,7 +932,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kWarps == 8 ? EXP_MINB : 4)
           // the edges' logits have been read above, whichever matrix they are in
           if (lane < sl.edge_count) {
             const int32_t e = edge_index(sl, lane, a.vocab);
-            const Gradient grad(softmax_shift(r.st.m), r.g.k);
+            const Gradient grad(r.st.m, r.g.k, a.scale);
             dz[e] = from_float<T>(grad.of(to_float(z[e]), a.scale));
           }
           // the entries over the block's own values of the row
@@ -953,10 +1008,16 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   __syncthreads();
   h.mass = head.mass;
   for (int w = 0; w < kPlainThreads / 32; ++w) m = fmaxf(m, maxima[w]);
-  float s = 0.0f;
+  float s = 0.0f, tilt = 0.0f;
 #pragma unroll 8
-  for (uint32_t v = tid; v < V; v += step) s += exp_scaled(to_float(z[v]) - softmax_shift(m), a.scale);
-  const SoftmaxStat st = {m, unbiased_sum(group_sum<kPlainThreads>(s, parts))};
+  for (uint32_t v = tid; v < V; v += step) {
+    const float x = to_float(z[v]), e = softmax_term(x, m, a.scale);
+    s += e;
+    if (fabsf(x) < INFINITY) tilt = fmaf(e, (x - m) * a.scale.hi, tilt);
+  }
+  SoftmaxStat st = {m, unbiased_sum(group_sum<kPlainThreads>(s, parts))};
+  tilt = group_sum<kPlainThreads>(tilt, maxima) * (0.693147181f * (a.scale.lo / a.scale.hi));
+  if (fabsf(tilt) < INFINITY) st.s.lo += tilt;
   if (wid == 0) {
     RowResult r;
     r.st = st;
@@ -976,7 +1037,7 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   }
   if (!dz) return;
   __syncthreads();  // every entry's logit is read before the gradient may take its place
-  const Gradient grad(softmax_shift(r.st.m), r.g.k);
+  const Gradient grad(r.st.m, r.g.k, a.scale);
   for (uint32_t v = tid; v < V; v += step) {
     float d = grad.of(to_float(z[v]), a.scale);
     if (kMode == ROW_POLICY && static_cast<int32_t>(v) == h.label) d = r.g.at_label;
@@ -994,23 +1055,36 @@ thd_status_t done(cudaError_t e) {
   return THD_ERR_CUDA;
 }
 
-// Shared memory of an SM and what a block takes of it besides its buffers.
+// Shared memory of an SM and what a block takes of it besides its buffers: the
+// driver's 1 KiB and the static arrays.
 constexpr int64_t kSmShared = 228 * 1024;
-constexpr int64_t kBlockShared = 1024 + 2560;  // the driver's 1 KiB and the static arrays
-constexpr int64_t kBlockBudget = kSmShared / EXP_PER - kBlockShared;
+constexpr int64_t kBlockShared = 1024 + 2304;
+// for the buffers of each of n blocks on an SM
+constexpr int64_t block_budget(int n) { return kSmShared / n - kBlockShared; }
 // Below this a slice is not divided further for want of rows.
 constexpr int64_t kSmallestSlice = 8 * 1024;
+// Slices up to this are taken by blocks of 4 warps, larger ones by 8.
+constexpr int64_t kSmallSlice = 32 * 1024;
+// Rows a cluster takes at a time, where there are enough of them.
+constexpr int32_t kGroup = 4;
 
-template <typename T, int kMode, int kWarps>
-cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaStream_t s) {
-  auto* kernel = row_cluster_kernel<T, kMode, kWarps>;
+template <typename T, int kMode, int kWarps, int kPerSm>
+thd_status_t launch_cluster(const RowArgs& a, RingShape shape, int64_t slice, int64_t room, int64_t entries,
+                            cudaStream_t s) {
+  auto* kernel = row_cluster_kernel<T, kMode, kWarps, kPerSm>;
+  const int64_t chunk = kWarps * 32 * kVecsPerStep * kChunkSteps;  // vectors
+  shape.vecs = static_cast<int32_t>(slice);
+  shape.chunks = static_cast<int32_t>(std::max<int64_t>(1, (slice + chunk - 1) / chunk));
+  const int64_t fit = (room - entries) / std::max<int64_t>(16, slice * 16);
+  shape.buffers = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fit, kMaxChunks / shape.chunks)));
+  const size_t smem = static_cast<size_t>(shape.buffers * slice * 16 + entries);
   if (smem > 40 * 1024) {  // 48 KiB, the static arrays among them, need no leave
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess) return done(e);
   }
-  const int32_t cluster = shape.cluster;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + shape.group - 1) / shape.group) * shape.cluster);
   cfg.blockDim = dim3(kWarps * 32 + 96);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -1018,16 +1092,26 @@ cudaError_t launch_cluster(const RowArgs& a, RingShape shape, size_t smem, cudaS
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.x = shape.cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + shape.group - 1) / shape.group) * cluster);
+  cfg.numAttrs = shape.cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, shape);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return done(e == cudaSuccess ? cudaGetLastError() : e);
 }
 
+// How many blocks share a row, and an SM.
+//
+// Three blocks on an SM hide one another's waits (for logits, for the other
+// blocks of the cluster) better than two; a row shared by more blocks pays
+// more exchanges and more work per row.  Shares of the copy bandwidth, policy
+// loss over bf16 rows: vocabulary 32768, one block a row, three on an SM 85 %,
+// two 75 %; 65536, two a row, 88 and 80 %; 100352, three a row and an SM 79 %,
+// two a row and an SM 87 %; 151936, five a row and three an SM 80 %, three a
+// row and two an SM 82 %.  So two on an SM where that takes fewer a row.  The
+// log-probabilities alone, which write nothing, take three on an SM whenever
+// they fit (151936: 95 and 89 %).
 template <typename T, int kMode>
 thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
@@ -1035,28 +1119,29 @@ thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int sms = sm_count();
   // vectors of a block's slice when `cluster` blocks share the row
   const auto slice_of = [&](int32_t cluster) { return ((row + 15) / 16 + cluster - 1) / cluster; };
+  const auto least = [&](int64_t room) {
+    int32_t cluster = 1;
+    while (cluster <= kMaxCluster && slice_of(cluster) * 16 + entries > room) ++cluster;
+    return cluster;  // kMaxCluster + 1: none
+  };
+  const int32_t by3 = least(block_budget(3)), by2 = least(block_budget(2));
+  int32_t per_sm = by3 <= kMaxCluster && (kMode == ROW_SCORE || by3 <= by2) ? 3 : by2 <= kMaxCluster ? 2 : 1;
   RingShape shape;
-  shape.cluster = 1;
-  while (shape.cluster < kMaxCluster && EXP_ROWS * slice_of(shape.cluster) * 16 + entries > kBlockBudget) ++shape.cluster;
+  shape.cluster = per_sm == 3 ? by3 : per_sm == 2 ? by2 : kMaxCluster;
+  // few rows: more blocks for each, so that every SM has one
   while (shape.cluster < kMaxCluster && static_cast<int64_t>(a.rows) * (shape.cluster + 1) <= sms &&
          slice_of(shape.cluster + 1) * 16 >= kSmallestSlice)
     ++shape.cluster;
   const int64_t slice = slice_of(shape.cluster);
-  shape.group = EXP_G;
+  shape.group = kGroup;
   while (shape.group > 1 && static_cast<int64_t>(a.rows) * shape.cluster < 16ll * sms * shape.group) shape.group /= 2;
   if (slice * 16 + entries > kMaxSlice || static_cast<int64_t>(a.rows) * shape.cluster > INT32_MAX)
     return done(launch_pdl(row_plain_kernel<T, kMode>, dim3(static_cast<unsigned>(a.rows)), dim3(kPlainThreads),
                            static_cast<size_t>(entries / kJobs), s, a));
-  const int warps = slice <= 512 ? 4 : 8;
-  const int64_t step = warps * 32 * kVecsPerStep * kChunkSteps;
-  shape.vecs = static_cast<int32_t>(slice);
-  shape.chunks = static_cast<int32_t>(std::max<int64_t>(1, (slice + step - 1) / step));
-  const int64_t room = slice * 16 + entries <= kBlockBudget ? kBlockBudget : kMaxSlice;
-  const int64_t fit = ((warps == 4 ? kBlockBudget / 2 : room) - entries) / std::max<int64_t>(16, slice * 16);
-  shape.buffers = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(fit, kMaxChunks / shape.chunks)));
-  const size_t smem = static_cast<size_t>(shape.buffers * slice * 16 + entries);
-  if (warps == 4) return done(launch_cluster<T, kMode, 4>(a, shape, smem, s));
-  return done(launch_cluster<T, kMode, 8>(a, shape, smem, s));
+  if (slice * 16 <= kSmallSlice && slice * 16 + entries <= block_budget(4))
+    return launch_cluster<T, kMode, 4, 4>(a, shape, slice, block_budget(4), entries, s);
+  if (per_sm == 3) return launch_cluster<T, kMode, 8, 3>(a, shape, slice, block_budget(3), entries, s);
+  return launch_cluster<T, kMode, 8, 2>(a, shape, slice, per_sm == 2 ? block_budget(2) : kMaxSlice, entries, s);
 }
 
 template <typename T>
@@ -1100,10 +1185,13 @@ __global__ void __launch_bounds__(kBackThreads)
   // a row that takes no part: zeros, and its logits are not read
   const bool idle = up == 0.0f || bad || l == -INFINITY;
   const float g = up * a.grad_scale * a.scale.inv_tau;
-  // z/tau - lse = (z - top)/tau; what lse tau rounds off goes into the factor
-  const float top = l * a.scale.tau;
-  const float rest = fabsf(top) < INFINITY ? fmaf(-top, a.scale.inv_tau, l) : 0.0f;
-  const float k = -g * ex2(-rest * 1.44269504f);
+  // z/tau - lse = (z - top)/tau; what lse tau and top hi round off goes into the factor
+  const float top = l * a.scale.tau, x = top * a.scale.hi;
+  const bool far = softmax_far(top, a.scale);
+  float rest = fabsf(top) < INFINITY ? -1.44269504f * fmaf(-top, a.scale.inv_tau, l) : 0.0f;
+  if (fabsf(x) < INFINITY) rest -= fmaf(top, a.scale.hi, -x);
+  // of an infinite log-sum-exp every finite logit has probability 0; a NaN stays one
+  const float k = l == INFINITY ? 0.0f : l != l ? l : -g * ex2(rest);
   // the label's element is written again by the thread that wrote it, from
   // the logit read before
   int32_t writer = -1;
@@ -1114,11 +1202,11 @@ __global__ void __launch_bounds__(kBackThreads)
   }
   const float z_label = tid == writer ? to_float(z[label]) : 0.0f;
 
-  const Gradient grad(top, k);
+  const Gradient grad(top, k, a.scale);
   const auto gradient = [&](const uint4& v) { return grad.of<T>(v, a.scale); };
   const uint4 zeros = make_uint4(0, 0, 0, 0);
   T* dv = dz + lo_v;
-  if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0) {
+  if ((reinterpret_cast<uintptr_t>(dv) & 15u) == 0 && !far) {
     const uint4* from = reinterpret_cast<const uint4*>(z + lo_v) + tid;
     uint4* to = reinterpret_cast<uint4*>(dv) + tid;
     int32_t left = count - tid;
@@ -1132,10 +1220,10 @@ __global__ void __launch_bounds__(kBackThreads)
     for (; left > 0; left -= kBackThreads, from += kBackThreads, to += kBackThreads)
       *to = idle ? zeros : gradient(*from);
   } else {
-    // a gradient laid out to another alignment than the logits
+    // a gradient laid out to another alignment than the logits, or a far log-sum-exp
     const uint4* from = reinterpret_cast<const uint4*>(z + lo_v);
     for (int32_t i = tid; i < count; i += kBackThreads) {
-      const uint4 d = idle ? zeros : gradient(from[i]);
+      const uint4 d = idle ? zeros : grad.of_any<T>(from[i], a.scale);
 #pragma unroll
       for (int j = 0; j < N; ++j) Word<T>::store_elem(dv + static_cast<int64_t>(i) * N + j, d, j);
     }
@@ -1144,7 +1232,7 @@ __global__ void __launch_bounds__(kBackThreads)
     const int32_t e = edge_index(row, tid, a.vocab);
     dz[e] = from_float<T>(idle ? 0.0f : grad.of(to_float(z[e]), a.scale));
   }
-  if (tid == writer) dz[label] = from_float<T>(g + k * exp_scaled(z_label - top, a.scale));
+  if (tid == writer) dz[label] = from_float<T>(g + grad.of(z_label, a.scale));
 }
 
 template <typename T>
