@@ -1065,8 +1065,14 @@ constexpr int64_t block_budget(int n) { return kSmShared / n - kBlockShared; }
 constexpr int64_t kSmallestSlice = 8 * 1024;
 // Slices up to this are taken by blocks of 4 warps, larger ones by 8.
 constexpr int64_t kSmallSlice = 32 * 1024;
-// Rows a cluster takes at a time, where there are enough of them.
+// Rows a cluster takes at a time, where there are enough of them: the loads of
+// their scalars wait for one another (2 to 3 us), which a row shorter than
+// that would feel.  Rows of kLongRow bytes and a gradient take longer and are
+// taken one by one, for the balance (8192 rows of 151936 bf16, a third of them
+// without loss: 685 us, by fours 700; log-probabilities of 4096 such rows by
+// fours, with their gradient 448 us, one by one 457).
 constexpr int32_t kGroup = 4;
+constexpr int64_t kLongRow = 256 * 1024;
 
 template <typename T, int kMode, int kWarps, int kPerSm>
 thd_status_t launch_cluster(const RowArgs& a, RingShape shape, int64_t slice, int64_t room, int64_t entries,
@@ -1110,8 +1116,9 @@ thd_status_t launch_cluster(const RowArgs& a, RingShape shape, int64_t slice, in
 // two 75 %; 65536, two a row, 88 and 80 %; 100352, three a row and an SM 79 %,
 // two a row and an SM 87 %; 151936, five a row and three an SM 80 %, three a
 // row and two an SM 82 %.  So two on an SM where that takes fewer a row.  The
-// log-probabilities alone, which write nothing, take three on an SM whenever
-// they fit (151936: 95 and 89 %).
+// log-probabilities alone, which write nothing, take three on an SM wherever
+// they fit (131072: 98 and 88 %; 2049 rows of 50257 f16 with their backward
+// pass 90 and 99 us).
 template <typename T, int kMode>
 thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
@@ -1125,7 +1132,8 @@ thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
     return cluster;  // kMaxCluster + 1: none
   };
   const int32_t by3 = least(block_budget(3)), by2 = least(block_budget(2));
-  int32_t per_sm = by3 <= kMaxCluster && (kMode == ROW_SCORE || by3 <= by2) ? 3 : by2 <= kMaxCluster ? 2 : 1;
+  const bool two = by2 < by3 && (kMode != ROW_SCORE || by3 > kMaxCluster);
+  const int32_t per_sm = by2 > kMaxCluster ? 1 : two ? 2 : 3;
   RingShape shape;
   shape.cluster = per_sm == 3 ? by3 : per_sm == 2 ? by2 : kMaxCluster;
   // few rows: more blocks for each, so that every SM has one
@@ -1133,7 +1141,7 @@ thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
          slice_of(shape.cluster + 1) * 16 >= kSmallestSlice)
     ++shape.cluster;
   const int64_t slice = slice_of(shape.cluster);
-  shape.group = kGroup;
+  shape.group = kMode != ROW_SCORE && row >= kLongRow ? 1 : kGroup;
   while (shape.group > 1 && static_cast<int64_t>(a.rows) * shape.cluster < 16ll * sms * shape.group) shape.group /= 2;
   if (slice * 16 + entries > kMaxSlice || static_cast<int64_t>(a.rows) * shape.cluster > INT32_MAX)
     return done(launch_pdl(row_plain_kernel<T, kMode>, dim3(static_cast<unsigned>(a.rows)), dim3(kPlainThreads),
