@@ -147,7 +147,7 @@ SIGNATURES = {
     "thd_pack_docs_noalloc": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_int32, c_int32, c_int32, c_int32,
                                         c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
                                         c_void_p]),
-    "thd_loss_weights_workspace_bytes": (c_size_t, [c_int32]),
+    "thd_loss_weights_workspace_bytes": (c_size_t, [c_int32, c_int64]),
     "thd_loss_weights": (c_int32, [c_void_p, c_void_p, c_int32, c_int64, c_int32, c_int32, c_void_p, c_void_p,
                                    c_void_p, c_size_t, c_void_p, c_void_p]),
     "thd_token_logprobs": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),

@@ -83,8 +83,9 @@ using namespace thd;
 
 extern "C" {
 
-size_t thd_loss_weights_workspace_bytes(int32_t num_docs) {
-  return num_docs < 0 ? 0 : static_cast<size_t>(num_docs) * sizeof(int32_t);
+size_t thd_loss_weights_workspace_bytes(int32_t num_docs, int64_t T) {
+  if (num_docs < 0 || (T > 0 && T <= THD_LOSS_WEIGHTS_FEW_ROWS && num_docs <= THD_LOSS_WEIGHTS_FEW_DOCS)) return 0;
+  return static_cast<size_t>(num_docs) * sizeof(int32_t);
 }
 
 thd_status_t thd_loss_weights(const uint8_t* loss_mask, const int32_t* cu_seqlens_padded, int32_t num_docs, int64_t T,
@@ -94,7 +95,7 @@ thd_status_t thd_loss_weights(const uint8_t* loss_mask, const int32_t* cu_seqlen
   if (reduction != THD_TOKEN_MEAN && reduction != THD_DOC_MEAN && reduction != THD_TOKEN_SUM)
     return THD_ERR_INVALID_ARG;
   if (T > 0 && (!loss_mask || !weights)) return THD_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, workspace_bytes, thd_loss_weights_workspace_bytes(num_docs)))
+  if (!workspace_ok(workspace, workspace_bytes, thd_loss_weights_workspace_bytes(num_docs, T)))
     return THD_ERR_INVALID_ARG;
   return launch_loss_weights(loss_mask, cu_seqlens_padded, num_docs, static_cast<int32_t>(T), cp_size, reduction,
                              weights, doc_ids, static_cast<int32_t*>(workspace), d_status, stream);

@@ -143,9 +143,10 @@ def loss_weights(loss_mask, cu_seqlens_padded, cp: int = 1, reduction: int = TOK
     cu_p = _vector(cu_seqlens_padded, "cu_seqlens_padded", n + 1, torch.int32, dev)
     weights = _empty(T, torch.float32, loss_mask.device, stream)
     doc_ids = _empty(T, torch.int32, loss_mask.device, stream)
-    ws = _empty(n, torch.int32, loss_mask.device, stream)
+    nbytes = L.load().thd_loss_weights_workspace_bytes(n, T)
+    ws = _empty(nbytes, torch.uint8, loss_mask.device, stream) if nbytes else None
     _call("thd_loss_weights", dev, stream, status, loss_mask.data_ptr(), cu_p, n, T, cp, reduction,
-          weights.data_ptr(), doc_ids.data_ptr(), ws.data_ptr(), 4 * n)
+          weights.data_ptr(), doc_ids.data_ptr(), None if ws is None else ws.data_ptr(), nbytes)
     return weights, doc_ids
 
 

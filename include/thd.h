@@ -493,11 +493,15 @@ typedef enum thd_reduction {
  *  loss_mask   device uint8[T]
  *  weights     device float[T]
  *  doc_ids     device int32[T] or NULL
- *  workspace   device, >= thd_loss_weights_workspace_bytes(num_docs), 4-byte aligned
+ *  workspace   device, >= thd_loss_weights_workspace_bytes(num_docs, T), 4-byte aligned;
+ *              none is needed (NULL, 0) up to THD_LOSS_WEIGHTS_FEW_ROWS rows of
+ *              THD_LOSS_WEIGHTS_FEW_DOCS documents
  * Device checks of the boundaries as for thd_route_build (the divisibility
  * check when cp_size > 1).
  */
-size_t thd_loss_weights_workspace_bytes(int32_t num_docs);
+#define THD_LOSS_WEIGHTS_FEW_ROWS 2048
+#define THD_LOSS_WEIGHTS_FEW_DOCS 2048
+size_t thd_loss_weights_workspace_bytes(int32_t num_docs, int64_t T);
 thd_status_t thd_loss_weights(const uint8_t *loss_mask, const int32_t *cu_seqlens_padded, int32_t num_docs,
                               int64_t T, int32_t cp_size, int32_t reduction, float *weights, int32_t *doc_ids,
                               void *workspace, size_t workspace_bytes, int32_t *d_status,

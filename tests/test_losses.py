@@ -204,10 +204,11 @@ def test_host_checks_return_before_any_launch():
     assert distill(z(), None) == INV and distill(z(), teacher(), w=None) == INV
     assert distill(z(), teacher(), tl=None) == INV and distill(z(), teacher(), loss=None) == INV
 
-    def weights(mask=fake, cu=fake, n=2, T=8, cp=2, red=0, w=fake, docs=None, ws=fake, nb=8):
+    def weights(mask=fake, cu=fake, n=2, T=2052, cp=2, red=0, w=fake, docs=None, ws=fake, nb=8):
         return lib.thd_loss_weights(mask, cu, n, T, cp, red, w, docs, ws, nb, None, None)
 
-    assert lib.thd_loss_weights_workspace_bytes(2) == 8 and lib.thd_loss_weights_workspace_bytes(-1) == 0
+    size = lib.thd_loss_weights_workspace_bytes
+    assert size(2, 2048) == 0 and size(2, 2049) == 8 and size(2048, 8) == 0 and size(2049, 8) == 4 * 2049 and size(-1, 8) == 0
     for kw in (dict(mask=None), dict(cu=None), dict(n=-1), dict(T=-1), dict(T=1 << 31), dict(T=6), dict(cp=0), dict(cp=65),
                dict(red=3), dict(red=-1), dict(w=None), dict(ws=None), dict(nb=7), dict(ws=fake + 1)):
         assert weights(**kw) == INV, kw
@@ -325,7 +326,8 @@ def test_python_layer_refuses_shapes_and_types():
 
 @gpu
 @pytest.mark.parametrize("lengths,cp", [([1], 1), ([3, 0, 5, 1], 1), ([0, 0, 7], 1), ([4, 8, 0, 12], 2), ([16, 48, 16], 8),
-                                        ([12, 24], 3), ([1000, 37, 2051], 1), ([128 * 40, 64], 4), ([2] * 700, 1)])
+                                        ([12, 24], 3), ([1000, 37, 2051], 1), ([128 * 40, 64], 4), ([2] * 700, 1), ([1] * 2049, 1),
+                                        ([2000, 48], 1), ([2000, 49], 1), ([8 * 2000, 0, 8 * 301], 4)])
 @pytest.mark.parametrize("reduction", [thd.TOKEN_MEAN, thd.DOC_MEAN, thd.TOKEN_SUM])
 def test_loss_weights(lengths, cp, reduction):
     cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
