@@ -747,8 +747,8 @@ def test_no_rows_at_all():
 
 
 @gpu
-def test_repeated_runs_give_the_same_bits_on_another_stream_and_in_a_graph():
-    T, V = 300, 5003
+@pytest.mark.parametrize("T,V", [(300, 5003), (700, 70001), (9, 151936)])
+def test_repeated_runs_give_the_same_bits_on_another_stream_and_in_a_graph(T, V):
     z, _ = make_logits(4, T, V, BF16)
     y = torch.randint(0, V, (T,), device="cuda", dtype=torch.int32)
     want = [s(z) for s in _steps(z, y)]
@@ -827,6 +827,66 @@ def test_one_training_step_from_raw_rows(cp):
     same(pref.loss.item(), wp["loss"], 2e-6)
     same(pref.dlogprobs.cpu().numpy(), wp["dlogprobs"], 1e-6)
     same_gradient(d, O.token_logprobs_backward(zn, y.cpu().numpy(), wp["dlogprobs"]), BF16, np.full(T, 3e-6))
+
+
+@gpu
+def test_the_example_trains():
+    """examples/post_training_step.py: every loss falls, and what it runs on leaves no error."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "post_training_step.py")
+    spec = importlib.util.spec_from_file_location("post_training_step", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    losses = module.main(steps=8)
+    assert sorted(losses) == ["distillation", "policy", "preference"]
+    for name, values in losses.items():
+        assert np.isfinite(values).all() and values[-1] < values[0], (name, values)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", [(1200, 151936), (400, 40001), (3000, 12289)])
+def test_many_rows_at_once(T, V, dtype):
+    """Enough rows that every cluster takes several, with runs of rows without loss between them: each loss against torch
+    in 64 bits on a sample of the rows."""
+    if dtype == F32 and V == 151936:
+        T = 500
+    z = torch.randn(T, V, device="cuda", dtype=torch.float32, generator=torch.Generator("cuda").manual_seed(V)).mul_(2).to(dtype)
+    g = np.random.default_rng(V)
+    y = torch.from_numpy(g.integers(0, V, T)).cuda().to(torch.int32)
+    w = np.full(T, 1.0 / T)
+    for a in range(0, T, 37):
+        w[a:a + int(g.integers(0, 20))] = 0
+    w = dev(w, F32)
+    on = (w != 0).to(torch.uint8)
+    st = thd.new_status()
+    lp, lse = thd.token_logprobs(z, y, on, status=st)
+    ids = torch.from_numpy(g.integers(0, V, (T, 16))).cuda().to(torch.int32)
+    sc = dev(g.standard_normal((T, 16)), F32)
+    A = dev(g.standard_normal(T), F32)
+    pol = thd.policy_loss(z, y, w, lp - 0.1, A, ref_logprobs=lp + 0.2, clip_low=0.5, clip_high=0.5, kl_coef=0.1, status=st)
+    dis = thd.distill_topk_loss(z, ids, sc, w, status=st)
+    back = thd.token_logprobs_backward(z, y, lse, w, status=st)
+    thd.check_status(st)
+    pick = np.unique(np.concatenate([[0, T - 1], g.integers(0, T, 24)]))
+    zn, yn, wn = z[pick].double().cpu().numpy(), y.cpu().numpy()[pick], w.double().cpu().numpy()[pick]
+    want_lp, want_lse = O.token_logprobs(zn, yn, wn != 0)
+    lpn = lp.double().cpu().numpy()[pick]
+    same(lpn, want_lp, lp_tol(want_lp))
+    same(lse.cpu().numpy()[pick], want_lse, lp_tol(want_lse))
+    An = A.cpu().numpy()[pick]
+    want = O.policy_loss(zn, yn, wn, lpn - 0.1, An, ref=lpn + 0.2, clip_low=0.5, clip_high=0.5, kl_coef=0.1)
+    same_gradient(pol.dlogits[pick], want["dlogits"], dtype, wn * (8 * np.abs(An) + 1) * 1.6e-5)
+    want = O.distill_topk_loss(zn, ids.cpu().numpy()[pick], sc.double().cpu().numpy()[pick], wn)
+    same(dis.token_losses.cpu().numpy()[pick], want["token_losses"], 80 * 1e-6 + 5e-6)
+    same_gradient(dis.dlogits[pick], want["dlogits"], dtype, wn * 2 * 1.6e-5)
+    want = O.token_logprobs_backward(zn, yn, wn)
+    same_gradient(back[pick], want, dtype, wn * (8e-6 + 2.4e-7 * np.abs(want_lse)))
+    idle = w == 0
+    for d in (pol.dlogits, dis.dlogits, back):
+        assert not d[idle].any()
+    assert not lp[idle].any() and not lse[idle].any() and not dis.token_losses[idle].any()
 
 
 def test_oracle_is_exported():
