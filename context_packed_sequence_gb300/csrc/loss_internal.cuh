@@ -158,15 +158,17 @@ struct Teacher {
   int32_t* id;  // -1: absent
   float* q;     // probability; 0 for an absent entry
   float* lq;    // logarithm of it
+  float* z;     // the student's logit; later the gradient in the entry's place
 };
 
 __host__ __device__ __forceinline__ int32_t teacher_slots(int32_t count) { return (count + 3) & ~3; }
 __host__ __device__ __forceinline__ size_t teacher_bytes(int32_t count) {
-  return 3 * sizeof(float) * static_cast<size_t>(teacher_slots(count));
+  return 4 * sizeof(float) * static_cast<size_t>(teacher_slots(count));
 }
 __device__ __forceinline__ Teacher teacher_at(void* mem, int32_t count) {
   const int32_t n = teacher_slots(count);
-  return {static_cast<int32_t*>(mem), static_cast<float*>(mem) + n, static_cast<float*>(mem) + 2 * n};
+  float* const f = static_cast<float*>(mem);
+  return {static_cast<int32_t*>(mem), f + n, f + 2 * n, f + 3 * n};
 }
 
 __device__ __forceinline__ float teacher_score(const RowArgs& a, int64_t i) {

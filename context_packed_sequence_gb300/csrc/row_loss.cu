@@ -280,12 +280,22 @@ struct RowResult {
   bool idle;       // the row takes no part after all
 };
 
-// The loss terms of the teacher's entries for which `mine(id)`, entry by entry
-// from `first` in steps of `step`; `logit(id)` reads the row.  Leaves the
-// gradient in the entry's place in te.lq and returns the loss / tau^2.
+// The logits of the teacher's entries for which `mine(id)`, entry by entry from
+// `first` in steps of `step`; `logit(id)` reads the row.
 template <class Mine, class Logit>
+__device__ __forceinline__ void read_entries(const RowArgs& a, const Teacher& te, int32_t first, int32_t step, Mine mine,
+                                             Logit logit) {
+  for (int32_t k = first; k < a.teacher_count; k += step) {
+    const int32_t id = te.id[k];
+    if (id >= 0 && mine(id)) te.z[k] = logit(id);
+  }
+}
+
+// Their loss terms: leaves the gradient in each one's place in te.z and returns
+// the loss / tau^2.
+template <class Mine>
 __device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher& te, const RowHead& h, SoftmaxStat st,
-                                                 int32_t first, int32_t step, Mine mine, Logit logit) {
+                                                 int32_t first, int32_t step, Mine mine) {
   const RowNorm norm = row_norm(st, a.scale);
   const float gs = a.grad_scale * h.weight * a.scale.tau;
   const bool empty = stat_is_empty(st);
@@ -293,9 +303,9 @@ __device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher
   for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
     if (id < 0 || !mine(id)) continue;
-    const Pair lp = entry_logprob(logit(id), empty, norm, a.scale);
+    const Pair lp = entry_logprob(te.z[k], empty, norm, a.scale);
     if (te.q[k] != 0.0f) loss += te.q[k] * ((te.lq[k] - lp.hi) - lp.lo);
-    te.lq[k] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
+    te.z[k] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
   }
   return loss;
 }
@@ -305,7 +315,7 @@ __device__ __forceinline__ void write_entries(const RowArgs& a, const Teacher& t
                                               Mine mine) {
   for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
-    if (id >= 0 && mine(id)) dz[id] = from_float<T>(te.lq[k]);
+    if (id >= 0 && mine(id)) dz[id] = from_float<T>(te.z[k]);
   }
 }
 
@@ -872,8 +882,9 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
     }
   } else {
     // ---- finishing rows
-    int32_t b = 0;
-    uint32_t got = 0;  // rows with weight so far
+    int32_t b = 0;       // ROW_DISTILL: buffer of the next row with weight
+    uint32_t phase = 0;  // and of the ring
+    uint32_t got = 0;    // rows with weight so far
     for (int32_t k = 0;; ++k) {
       const int32_t slot = k % kJobs;
       if (!wait_or_quit(&job_full[slot], (k / kJobs) & 1, &quit)) break;
@@ -917,7 +928,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
           const int32_t in_slice = h.label - lo_v;
           r.writer = in_slice / N % kThreads;
           if (in_slice < 0) r.writer = h.label;                                            // the head
-          else if (h.label >= hi_v) r.writer = sl.edge_count - (a.vocab - h.label);  // the tail
+          else if (h.label >= hi_v) r.writer = sl.edge_count - (a.vocab - h.label);        // the tail
         }
       }
       __syncwarp();
@@ -933,14 +944,21 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
         const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
         const T* const held = reinterpret_cast<const T*>(ring + b * shape.vecs);
         const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
-        const float part = warp_sum(teacher_entries(a, te, h, r.st, lane, 32, mine, logit));
+        // the copies have landed, as the statistics show; this warp has to see it for itself
+        bool ok = true;
+        for (int j = 0; ok && j < shape.chunks; ++j) ok = wait_or_quit(&full[b * shape.chunks + j], phase, &quit);
+        if (!ok) break;
+        read_entries(a, te, lane, 32, mine, logit);
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0)
           for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&empty[b * shape.chunks + j]);
-          if (cluster > 1)
-            cluster_send(&loss_box[got % kJobs][rank], &loss_bar[got % kJobs], 0, make_float2(part, 0.0f));
+        if (++b == shape.buffers) {
+          b = 0;
+          phase ^= 1u;
         }
-        if (++b == shape.buffers) b = 0;
+        const float part = warp_sum(teacher_entries(a, te, h, r.st, lane, 32, mine));
+        if (cluster > 1 && lane == 0)
+          cluster_send(&loss_box[got % kJobs][rank], &loss_bar[got % kJobs], 0, make_float2(part, 0.0f));
         if (a.dlogits) {
           T* const dz = static_cast<T*>(a.dlogits) + t * a.dstride;
           // the edges' logits have been read above, whichever matrix they are in
@@ -1046,7 +1064,8 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   const auto all = [](int32_t) { return true; };
   if (kMode == ROW_DISTILL) {
     const auto logit = [&](int32_t id) { return to_float(z[id]); };
-    const float part = group_sum<kPlainThreads>(teacher_entries(a, te, h, r.st, tid, kPlainThreads, all, logit), parts);
+    read_entries(a, te, tid, kPlainThreads, all, logit);
+    const float part = group_sum<kPlainThreads>(teacher_entries(a, te, h, r.st, tid, kPlainThreads, all), parts);
     if (tid == 0) a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
   }
   if (!dz) return;
