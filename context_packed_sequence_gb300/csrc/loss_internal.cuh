@@ -56,7 +56,7 @@ struct RowHead {
   float z_label;
   float old_lp, ref_lp, advantage;
   int32_t label;
-  int32_t fetched;  // the row had weight (and its label may be bad)
+  int32_t repeats;  // ROW_DISTILL: an id comes more than once
 };
 
 template <typename T, int kMode>
@@ -65,7 +65,6 @@ __device__ __forceinline__ RowHead row_head(const RowArgs& a, int64_t t) {
   h.label = -1;
   if (kMode == ROW_SCORE) h.weight = (!a.mask || a.mask[t]) ? 1.0f : 0.0f;
   else h.weight = a.weights[t];
-  h.fetched = h.weight != 0.0f;
   if (h.weight == 0.0f || kMode == ROW_DISTILL) return h;
   h.label = a.labels[t];
   bool ok = h.label >= 0 && h.label < a.vocab;
@@ -160,6 +159,8 @@ struct Teacher {
   float* lq;    // logarithm of it
   float* z;     // the student's logit; later the gradient in the entry's place
 };
+constexpr int kEntryBatch = 4;  // loads of each kind in flight a lane
+constexpr int kHashRounds = 6;  // 1024 different ids: 0.2, 0.02 and 1e-4 of them are left after 1, 2 and 3
 
 __host__ __device__ __forceinline__ int32_t teacher_slots(int32_t count) { return (count + 3) & ~3; }
 __host__ __device__ __forceinline__ size_t teacher_bytes(int32_t count) {
@@ -171,10 +172,15 @@ __device__ __forceinline__ Teacher teacher_at(void* mem, int32_t count) {
   return {static_cast<int32_t*>(mem), f + n, f + 2 * n, f + 3 * n};
 }
 
-__device__ __forceinline__ float teacher_score(const RowArgs& a, int64_t i) {
-  if (a.teacher_dtype == THD_DTYPE_BF16) return to_float(static_cast<const __nv_bfloat16*>(a.teacher_scores)[i]);
-  if (a.teacher_dtype == THD_DTYPE_F16) return to_float(static_cast<const __half*>(a.teacher_scores)[i]);
-  return static_cast<const float*>(a.teacher_scores)[i];
+// A score as its bits, and the bits as a float.
+__device__ __forceinline__ uint32_t teacher_bits(const RowArgs& a, int64_t i) {
+  if (a.teacher_dtype == THD_DTYPE_F32) return static_cast<const uint32_t*>(a.teacher_scores)[i];
+  return static_cast<const unsigned short*>(a.teacher_scores)[i];
+}
+__device__ __forceinline__ float teacher_score(const RowArgs& a, uint32_t bits) {
+  if (a.teacher_dtype == THD_DTYPE_F32) return __uint_as_float(bits);
+  if (a.teacher_dtype == THD_DTYPE_BF16) return __uint_as_float(bits << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -188,20 +194,82 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Whether an id of the row comes more than once (or, hardly ever, may do); by
+// one whole warp.  Every entry writes its number to a place that its id is
+// hashed to, in the memory of z, which is filled later, and reads back whose
+// number stayed: its own, another one's with the same id, or that of another
+// id, which it tries elsewhere.  Entries with one id go the same way, so one
+// of them finds the other.  Comparing each with each instead took 0.6 us a
+// row for 64 entries and 40 us for 512.
+__device__ __forceinline__ bool ids_repeat(const Teacher& s, int32_t count) {
+  const int lane = threadIdx.x & 31;
+  if (count <= 32) {
+    const int32_t id = lane < count ? s.id[lane] : -1;
+    return __any_sync(kFullMask, (__match_any_sync(kFullMask, id) & ((1u << lane) - 1)) != 0 && id >= 0);
+  }
+  const uint32_t places = 2u * static_cast<uint32_t>(teacher_slots(count));
+  volatile unsigned short* const winner = reinterpret_cast<unsigned short*>(s.z);
+  uint32_t open = 0;  // bit i: entry 32 i + lane has not met its place
+  int i = 0;
+#pragma unroll 1
+  for (int32_t k = lane; k < count; k += 32, ++i) open |= (s.id[k] >= 0 ? 1u : 0u) << i;
+  bool repeat = false;
+  uint32_t factor = 0x9e3779b1u;
+#pragma unroll 1
+  for (int round = 0; round < kHashRounds && __any_sync(kFullMask, open != 0); ++round, factor += 0x3c6ef372u) {
+#pragma unroll 1
+    for (uint32_t left = open; left; left &= left - 1) {
+      const int32_t k = 32 * (__ffs(left) - 1) + lane;
+      winner[__umulhi(static_cast<uint32_t>(s.id[k]) * factor, places)] = static_cast<unsigned short>(k);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (uint32_t left = open; left; left &= left - 1) {
+      const int32_t k = 32 * (__ffs(left) - 1) + lane;
+      const int32_t id = s.id[k], w = winner[__umulhi(static_cast<uint32_t>(id) * factor, places)];
+      if (w != k) repeat |= s.id[w] == id;
+      if (w == k) open &= ~(left & (0u - left));
+    }
+    if (__any_sync(kFullMask, repeat)) return true;
+  }
+  return __any_sync(kFullMask, open != 0);
+}
+
 // Filled by one whole warp; `report`: this caller tells of bad ids.  Returns
-// the sum of the probabilities.
-__device__ __forceinline__ float load_teacher(const RowArgs& a, int64_t t, const Teacher& s, bool report) {
+// the sum of the probabilities and whether ids repeat.  Its loops are kept
+// short: unrolled, they push the code of the warps that compute out of the
+// instruction cache (4096 rows of 151936 bf16 with one entry: 434 and 421 us).
+__device__ __forceinline__ RowHead load_teacher(const RowArgs& a, int64_t t, const Teacher& s, bool report) {
   const int lane = threadIdx.x & 31, K = a.teacher_count;
   const int64_t base = t * K;
+  uint32_t* const bits = reinterpret_cast<uint32_t*>(s.lq);
+#pragma unroll 1
+  for (int k0 = lane; k0 < K; k0 += 32 * kEntryBatch) {
+    int32_t id[kEntryBatch];
+    uint32_t v[kEntryBatch];
+#pragma unroll
+    for (int j = 0; j < kEntryBatch; ++j) {
+      const int k = min(k0 + 32 * j, K - 1);
+      id[j] = a.teacher_ids[base + k];
+      v[j] = teacher_bits(a, base + k);
+    }
+#pragma unroll
+    for (int j = 0; j < kEntryBatch; ++j) {
+      const int k = k0 + 32 * j;
+      if (k >= K) break;
+      s.id[k] = id[j];
+      bits[k] = v[j];
+    }
+  }
   float top = -INFINITY;
   bool bad = false;
+#pragma unroll 1
   for (int k = lane; k < K; k += 32) {
-    const int32_t id = a.teacher_ids[base + k];
-    float v = teacher_score(a, base + k);
-    bad |= id >= a.vocab;
+    const int32_t id = s.id[k];
     const bool here = id >= 0 && id < a.vocab;
+    bad |= id >= a.vocab;
+    const float v = here ? teacher_score(a, bits[k]) : -INFINITY;
     s.id[k] = here ? id : -1;
-    if (!here) v = -INFINITY;
     s.lq[k] = v;
     top = fmaxf(top, v);
   }
@@ -211,12 +279,14 @@ __device__ __forceinline__ float load_teacher(const RowArgs& a, int64_t t, const
     top = warp_max(top);
     if (!(fabsf(top) < INFINITY)) top = 0.0f;
     float sum = 0.0f;
+#pragma unroll 1
     for (int k = lane; k < K; k += 32) sum += exp_scaled(s.lq[k] - top, a.scale);
     sum = warp_sum(sum);
     // without any entry every score stays -inf
     norm = sum == 0.0f ? 0.0f : logf(sum);
   }
   float mass = 0.0f;
+#pragma unroll 1
   for (int k = lane; k < K; k += 32) {
     float v = s.lq[k];
     if (a.normalize) v = (v - top) * a.scale.inv_tau - norm;
@@ -229,13 +299,18 @@ __device__ __forceinline__ float load_teacher(const RowArgs& a, int64_t t, const
     s.id[k] = -1;
     s.q[k] = 0.0f;
   }
-  return warp_sum(mass);
+  __syncwarp();
+  RowHead h = {};
+  h.mass = warp_sum(mass);
+  h.repeats = ids_repeat(s, K);
+  return h;
 }
 
-// Sum of the probabilities of the entries with this id (an id may come more
-// than once), four entries a step.
+// Sum of the probabilities of the entries with this id, four entries a step,
+// where ids repeat.
 __device__ __forceinline__ float entry_mass(const Teacher& s, int32_t id, int32_t count) {
   float q = 0.0f;
+#pragma unroll 1
   for (int32_t i = 0; i < teacher_slots(count); i += 4) {
     const int4 d = *reinterpret_cast<const int4*>(s.id + i);
     const float4 v = *reinterpret_cast<const float4*>(s.q + i);

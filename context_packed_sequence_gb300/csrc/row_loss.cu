@@ -287,6 +287,7 @@ struct RowResult {
 template <class Mine, class Logit>
 __device__ __forceinline__ void read_entries(const RowArgs& a, const Teacher& te, int32_t first, int32_t step,
                                              Mine mine, Logit logit) {
+#pragma unroll 1
   for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
     if (id >= 0 && mine(id)) te.z[k] = logit(id);
@@ -302,12 +303,14 @@ __device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher
   const float gs = a.grad_scale * h.weight * a.scale.tau;
   const bool empty = stat_is_empty(st);
   float loss = 0.0f;
+#pragma unroll 1
   for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
     if (id < 0 || !mine(id)) continue;
     const Pair lp = entry_logprob(te.z[k], empty, norm, a.scale);
     if (te.q[k] != 0.0f) loss += te.q[k] * ((te.lq[k] - lp.hi) - lp.lo);
-    te.z[k] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - entry_mass(te, id, a.teacher_count));
+    const float q = h.repeats ? entry_mass(te, id, a.teacher_count) : te.q[k];
+    te.z[k] = empty ? 0.0f : gs * (h.mass * expf(lp.hi + lp.lo) - q);
   }
   return loss;
 }
@@ -315,6 +318,7 @@ __device__ __forceinline__ float teacher_entries(const RowArgs& a, const Teacher
 template <typename T, class Mine>
 __device__ __forceinline__ void write_entries(const RowArgs& a, const Teacher& te, T* dz, int32_t first, int32_t step,
                                               Mine mine) {
+#pragma unroll 1
   for (int32_t k = first; k < a.teacher_count; k += step) {
     const int32_t id = te.id[k];
     if (id >= 0 && mine(id)) dz[id] = from_float<T>(te.z[k]);
@@ -698,18 +702,12 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
             continue;
           }
           ExpSum sum;
-          if (left + lane >= kStep) {
 #pragma unroll
-            for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], neg_shift, a.scale);
-          } else {  // as many as the warp has
-#pragma unroll
-            for (int u = 0; u < kVecsPerStep; ++u)
-              if (left + lane > u * kThreads) sum.template add<T>(v[u], neg_shift, a.scale);
-          }
+          for (int u = 0; u < kVecsPerStep; ++u) sum.template add<T>(v[u], neg_shift, a.scale);
           s.hi += sum.total();
           tilt += sum.tilt;
         }
-        if (kMode == ROW_SCORE) {
+        if (kMode == ROW_SCORE || !dz) {  // read once
           __syncwarp();
           if (lane == 0) mbar_arrive(&freed[j]);
         }
@@ -735,14 +733,14 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
       }
       ++sent;
 
-      if (kMode != ROW_SCORE) {
+      if (kMode != ROW_SCORE && dz) {
         // the gradient
         if (!wait_or_quit(&result_full[slot], parity, &quit)) break;
         const RowResult& r = results[slot];
         if (r.stop) break;
         T* const dv = dz + (sl.head + sl.first * N);
         const Gradient grad(r.st.m, r.g.k, a.scale);
-        if (dz && !r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0 && !softmax_far(r.st.m, a.scale)) {
+        if (!r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0 && !softmax_far(r.st.m, a.scale)) {
           uint4* to = reinterpret_cast<uint4*>(dv) + tid;
           from = buf + tid;
           left = mine;
@@ -756,23 +754,22 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
 #pragma unroll
                 for (int u = 0; u < kVecsPerStep; ++u) to[u * kThreads] = grad.template of<T>(v[u], a.scale);
               } else {
-#pragma unroll
-                for (int u = 0; u < kVecsPerStep; ++u)
-                  if (left > u * kThreads) to[u * kThreads] = grad.template of<T>(from[u * kThreads], a.scale);
+#pragma unroll 1
+                for (int i = 0; i < left; i += kThreads) to[i] = grad.template of<T>(from[i], a.scale);
               }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&freed[j]);
           }
         } else {
-          // no gradient, zeros, one laid out to another alignment than the logits, or a far maximum
-          if (dz && r.idle) zero_slice<T, kThreads>(dz, sl, a.vocab);
-          else if (dz) any_gradient<T, kThreads>(dv, buf, count, grad, a.scale);
+          // zeros, a gradient laid out to another alignment than the logits, or a far maximum
+          if (r.idle) zero_slice<T, kThreads>(dz, sl, a.vocab);
+          else any_gradient<T, kThreads>(dv, buf, count, grad, a.scale);
           __syncwarp();
           if (lane == 0)
             for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&freed[j]);
         }
-        if (dz && !r.idle) {
+        if (!r.idle) {
           if (kMode == ROW_POLICY && tid < sl.edge_count)
             dz[edge_index(sl, tid, a.vocab)] = from_float<T>(grad.of(edge, a.scale));
           // over the value just written, by the thread that wrote it
@@ -866,8 +863,11 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
         __syncwarp();
         if (kMode == ROW_DISTILL && __shfl_sync(kFullMask, job.fetched, j)) {
           const Teacher te = teacher_at(teachers + slot * teacher_bytes(a.teacher_count), a.teacher_count);
-          const float mass = load_teacher(a, first + j, te, rank == 0);
-          if (lane == j) h.mass = mass;
+          const RowHead loaded = load_teacher(a, first + j, te, rank == 0);
+          if (lane == j) {
+            h.mass = loaded.mass;
+            h.repeats = loaded.repeats;
+          }
         }
         __syncwarp();
         if (lane == j) {
@@ -1035,8 +1035,11 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   }
   const Teacher te = teacher_at(dynamic, a.teacher_count);
   if (kMode == ROW_DISTILL && wid == 0) {
-    h.mass = load_teacher(a, t, te, true);
-    if (lane == 0) head.mass = h.mass;
+    const RowHead loaded = load_teacher(a, t, te, true);
+    if (lane == 0) {
+      head.mass = loaded.mass;
+      head.repeats = loaded.repeats;
+    }
   }
   float m = -INFINITY;
 #pragma unroll 8
@@ -1045,6 +1048,7 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   if (lane == 0) maxima[wid] = m;
   __syncthreads();
   h.mass = head.mass;
+  h.repeats = head.repeats;
   for (int w = 0; w < kPlainThreads / 32; ++w) m = fmaxf(m, maxima[w]);
   float s = 0.0f, tilt = 0.0f;
 #pragma unroll 8

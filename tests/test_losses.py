@@ -623,6 +623,48 @@ def test_distill(T, V, stride, offset, dtype, K, normalize):
 
 
 @gpu
+@pytest.mark.parametrize("K", [2, 31, 64, 257, 1024])
+@pytest.mark.parametrize("V", [4096, 50257])
+def test_distill_repeated_ids_are_one_entry_of_the_gradient(K, V):
+    """Rows whose ids all differ, one id given twice (at either end, beside each other), one id given K times, and ids of which
+    many fall on one another's places whatever they are hashed with (0, 1, 2, ...); tolerances as in test_distill."""
+    g = np.random.default_rng(K + V)
+    T, tau = 6, 0.75
+    z, zn = make_logits(K, T, V, F32)
+    ids = np.stack([g.permutation(V)[:K] for _ in range(T)])
+    ids[1, -1] = ids[1, 0]
+    ids[2, K // 2] = ids[2, K // 2 - 1]
+    ids[3] = V - 1
+    ids[4] = np.arange(K)
+    ids[5] = np.arange(K)[::-1] * (V // K)
+    ids[5, ::3] = -1
+    scores = (g.standard_normal((T, K)) * 2).astype(np.float32)
+    w = np.abs(g.standard_normal(T)).astype(np.float32)
+    out = thd.distill_topk_loss(z, dev(ids, torch.int32), dev(scores, F32), dev(w, F32), temperature=tau)
+    want = O.distill_topk_loss(zn, ids, scores.astype(np.float64), w, tau, True)
+    same(out.token_losses.cpu().numpy(), want["token_losses"], tau * tau * 2 * 40 * 1e-6 + 5e-6)
+    same_gradient(out.dlogits, want["dlogits"], F32, w * tau * 2 * 1.6e-5)
+
+
+@gpu
+@pytest.mark.parametrize("T,V,dtype", [(700, 151936, BF16), (300, 50257, F16), (900, 4096, F32)])
+def test_the_loss_alone_is_the_loss_with_a_gradient(T, V, dtype):
+    """Over many rows, some without loss: the same bits with and without the gradient, and the logits stay."""
+    z, _ = make_logits(T, T, V, dtype)
+    g = np.random.default_rng(V)
+    f = lambda a: dev(a, F32)  # noqa: E731
+    w = g.random(T) * (g.random(T) < 0.7)
+    y, old, A = dev(g.integers(0, V, T), torch.int32), f(g.standard_normal(T) - 8), f(g.standard_normal(T))
+    ids, sc = dev(g.integers(0, V, (T, 40)), torch.int32), f(g.standard_normal((T, 40)))
+    keep = z.clone()
+    for call in (lambda **kw: thd.policy_loss(z, y, f(w), old, A, **kw)[:4],
+                 lambda **kw: thd.distill_topk_loss(z, ids, sc, f(w), **kw)[:2]):
+        for a, b in zip(call(), call(need_dlogits=False)):
+            assert torch.equal(a, b)
+    assert torch.equal(z, keep)
+
+
+@gpu
 def test_distill_gradient_is_the_losses_difference():
     """As for the policy loss: a directional difference within 2e-3."""
     T, V, K = 6, 300, 12
