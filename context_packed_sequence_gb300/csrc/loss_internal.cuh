@@ -43,11 +43,6 @@ struct RowArgs {
   int32_t teacher_dtype, teacher_count, normalize;
 };
 
-// dz_v = k * the row's term of z_v (SoftmaxStat), and `at_label` in the label's place
-struct RowGrad {
-  float k, at_label;
-};
-
 // What one row needs besides its logits; read by one thread, before the row's
 // statistics are known.
 struct RowHead {
@@ -112,40 +107,55 @@ __device__ __forceinline__ void write_score(const RowArgs& a, int64_t t, const R
   a.lse[t] = log_sum_exp(r, a.scale);
 }
 
-// Clipped policy loss of one row (formulas in include/thd.h) and the
-// coefficients of its gradient.  The ratio and the KL term take the
-// log-probability as a pair: its difference to old_lp and ref_lp is small,
-// and rounding it first would cost that difference about 5e-7.
-__device__ __forceinline__ RowGrad policy_row(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st,
-                                              bool write) {
-  const RowNorm r = row_norm(st, a.scale);
-  const Pair lp = label_logprob(h.z_label, st, r, a.scale);
-  const float ratio = expf((lp.hi - h.old_lp) + lp.lo);
+// Clipped policy loss of one row (formulas in include/thd.h).  The ratio and
+// the KL term take the log-probability as a pair: its difference to old_lp and
+// ref_lp is small, and rounding it first would cost that difference about 5e-7.
+struct PolicyTerms {
+  Pair lp;
+  float loss, kl;
+  bool clipped;
+  float g;  // d loss / d z_v = g (1[v = label] - p_v), scaled; 0 for an empty row
+};
+
+__device__ __forceinline__ PolicyTerms policy_terms(const RowArgs& a, const RowHead& h, SoftmaxStat st) {
+  PolicyTerms p;
+  p.lp = label_logprob(h.z_label, st, row_norm(st, a.scale), a.scale);
+  const float ratio = expf((p.lp.hi - h.old_lp) + p.lp.lo);
   // comparisons, not min/max: a NaN ratio stays one
   const float bounded = ratio < a.ratio_min ? a.ratio_min : (ratio > a.ratio_max ? a.ratio_max : ratio);
   const float gain = ratio * h.advantage, bounded_gain = bounded * h.advantage;
-  const bool clipped = gain > bounded_gain;
-  float loss = -(clipped ? bounded_gain : gain), slope = clipped ? 0.0f : -gain, kl = 0.0f;
+  p.clipped = gain > bounded_gain;
+  p.loss = -(p.clipped ? bounded_gain : gain);
+  p.kl = 0.0f;
+  float slope = p.clipped ? 0.0f : -gain;
   if (a.ref_logprobs) {
-    const float gap = (h.ref_lp - lp.hi) - lp.lo;
+    const float gap = (h.ref_lp - p.lp.hi) - p.lp.lo;
     const float em1 = expm1f(gap);
-    kl = em1 - gap;
+    p.kl = em1 - gap;
     if (a.kl_coef != 0.0f) {
-      loss = fmaf(a.kl_coef, kl, loss);
+      p.loss = fmaf(a.kl_coef, p.kl, p.loss);
       slope = fmaf(-a.kl_coef, em1, slope);
     }
   }
-  if (write) {
-    const int64_t T = a.rows;
-    a.logprobs[t] = lp.hi + lp.lo;
-    a.terms[t] = h.weight * loss;
-    a.terms[T + t] = h.weight * kl;
-    a.terms[2 * T + t] = clipped ? h.weight : 0.0f;
-  }
-  // d loss / d z_v = w slope (1[v = label] - p_v) / tau
-  const float g = a.grad_scale * h.weight * slope * a.scale.inv_tau;
-  if (stat_is_empty(st)) return {0.0f, 0.0f};
-  return {-g / st.s.hi, -g * expm1f(lp.hi)};
+  p.g = stat_is_empty(st) ? 0.0f : a.grad_scale * h.weight * slope * a.scale.inv_tau;
+  return p;
+}
+
+__device__ __forceinline__ void write_policy(const RowArgs& a, int64_t t, const RowHead& h, const PolicyTerms& p) {
+  const int64_t T = a.rows;
+  a.logprobs[t] = p.lp.hi + p.lp.lo;
+  a.terms[t] = h.weight * p.loss;
+  a.terms[T + t] = h.weight * p.kl;
+  a.terms[2 * T + t] = p.clipped ? h.weight : 0.0f;
+}
+
+// The factor of a row's terms (SoftmaxStat) in its gradient, and the gradient
+// in the label's place.
+__device__ __forceinline__ float policy_factor(const PolicyTerms& p, SoftmaxStat st) {
+  return p.g == 0.0f ? 0.0f : -p.g / st.s.hi;
+}
+__device__ __forceinline__ float policy_at_label(const PolicyTerms& p) {
+  return p.g == 0.0f ? 0.0f : -p.g * expm1f(p.lp.hi);
 }
 
 // ---------------------------------------------------------------------------

@@ -273,13 +273,11 @@ __device__ __forceinline__ void group_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 
-// A row's gradient as its threads need it, from the first warp to the block.
-struct RowResult {
-  SoftmaxStat st;
-  RowGrad g;
-  int32_t writer;  // the thread that wrote the label's place and writes it again; -1: none here
-  bool stop;       // something failed: nothing more is written
-  bool idle;       // the row takes no part after all
+// What the warps that write a row's gradient need of it.
+struct __align__(16) RowResult {
+  float m, k;    // dz_v = k * the term of z_v (SoftmaxStat)
+  int32_t stop;  // something failed: nothing more is written
+  int32_t idle;  // the row takes no part after all
 };
 
 // The logits of the teacher's entries for which `mine(id)`, entry by entry from
@@ -337,17 +335,8 @@ __device__ __forceinline__ float group_sum(float v, float* tmp) {
   return v;
 }
 
-// The scalars of a row and the coefficients of its gradient, from its
-// statistics; by a whole warp, `write`: this block reports them.
-template <int kMode>
-__device__ __forceinline__ RowGrad finish_row(const RowArgs& a, int64_t t, const RowHead& h, SoftmaxStat st,
-                                              bool write) {
-  if (kMode == ROW_SCORE) {
-    if (write) write_score(a, t, h, st);
-    return {0.0f, 0.0f};
-  }
-  if (kMode == ROW_POLICY) return policy_row(a, t, h, st, write);
-  return {stat_is_empty(st) ? 0.0f : a.grad_scale * h.weight * a.scale.tau * h.mass / st.s.hi, 0.0f};
+__device__ __forceinline__ float distill_factor(const RowArgs& a, const RowHead& h, SoftmaxStat st) {
+  return stat_is_empty(st) ? 0.0f : a.grad_scale * h.weight * a.scale.tau * h.mass / st.s.hi;
 }
 
 // ---------------------------------------------------------------------------
@@ -575,7 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ uint64_t full[kMaxChunks], empty[kMaxChunks];  // of each chunk of each buffer
   __shared__ uint64_t job_full[kJobs], job_empty[kJobs], head_full[kJobs], result_full[kJobs];
-  __shared__ uint64_t written[kMode == ROW_DISTILL ? kJobs : 1], loss_bar[kMode == ROW_DISTILL ? kJobs : 1];
+  __shared__ uint64_t written[kJobs], loss_bar[kMode == ROW_DISTILL ? kJobs : 1];
   __shared__ uint64_t stat_bar[2], next_full[2], next_free[2];
   __shared__ __align__(16) float4 next[2];               // answers to requests for rows
   __shared__ float2 inbox[2][kMaxCluster * kWarps];      // each warp's statistics of a row
@@ -601,8 +590,8 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
       mbar_init(&job_empty[i], kWarps + 2);
       mbar_init(&head_full[i], 1);
       mbar_init(&result_full[i], 1);
+      mbar_init(&written[i], kWarps);
       if (kMode == ROW_DISTILL) {
-        mbar_init(&written[i], kWarps);
         mbar_init(&loss_bar[i], 1);
         if (cluster > 1 && rank == 0) mbar_arrive_expect_tx(&loss_bar[i], 8 * cluster);
       }
@@ -643,7 +632,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
         if (dz) zero_slice<T, kThreads>(dz, sl, a.vocab);
         __syncwarp();
         if (lane == 0) {
-          if (kMode == ROW_DISTILL) mbar_arrive(&written[slot]);
+          if (kMode != ROW_SCORE) mbar_arrive(&written[slot]);
           mbar_arrive(&job_empty[slot]);
         }
         continue;
@@ -656,11 +645,12 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
 
       // The statistics: steps of a few vectors, their maximum first, so that
       // the sum's shift changes rarely, and for the whole warp at once.
-      float m = -INFINITY, edge = -INFINITY;
+      float m = -INFINITY;
       Pair s = {0.0f, 0.0f};
       float tilt = 0.0f;
       uint64_t neg_shift = 0;
       if (sl.edge_count > 0 && wid == 0) {
+        float edge = -INFINITY;
         if (lane < sl.edge_count)
           edge = to_float(static_cast<const T*>(a.logits)[job.row * a.stride + edge_index(sl, lane, a.vocab)]);
         m = warp_max_one(edge);
@@ -736,11 +726,11 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
       if (kMode != ROW_SCORE && dz) {
         // the gradient
         if (!wait_or_quit(&result_full[slot], parity, &quit)) break;
-        const RowResult& r = results[slot];
+        const RowResult r = results[slot];
         if (r.stop) break;
         T* const dv = dz + (sl.head + sl.first * N);
-        const Gradient grad(r.st.m, r.g.k, a.scale);
-        if (!r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0 && !softmax_far(r.st.m, a.scale)) {
+        const Gradient grad(r.m, r.k, a.scale);
+        if (!r.idle && (reinterpret_cast<uintptr_t>(dv) & 15u) == 0 && !softmax_far(r.m, a.scale)) {
           uint4* to = reinterpret_cast<uint4*>(dv) + tid;
           from = buf + tid;
           left = mine;
@@ -769,16 +759,10 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
           if (lane == 0)
             for (int j = 0; j < shape.chunks; ++j) mbar_arrive(&freed[j]);
         }
-        if (!r.idle) {
-          if (kMode == ROW_POLICY && tid < sl.edge_count)
-            dz[edge_index(sl, tid, a.vocab)] = from_float<T>(grad.of(edge, a.scale));
-          // over the value just written, by the thread that wrote it
-          if (kMode == ROW_POLICY && tid == r.writer) dz[heads[slot].label] = from_float<T>(r.g.at_label);
-        }
       }
       __syncwarp();
       if (lane == 0) {
-        if (kMode == ROW_DISTILL) mbar_arrive(&written[slot]);
+        if (kMode != ROW_SCORE) mbar_arrive(&written[slot]);
         mbar_arrive(&job_empty[slot]);
       }
       if (++b == shape.buffers) {
@@ -912,31 +896,24 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
       const int32_t n = cluster * kWarps;
       const float2 none = make_float2(-INFINITY, 0.0f);
       const float2 in0 = lane < n ? inbox[box][lane] : none, in1 = lane + 32 < n ? inbox[box][lane + 32] : none;
-      r.st.m = warp_max_one(fmaxf(in0.x, in1.x));
-      const Pair s0 = rescaled(in0.x, {in0.y, 0.0f}, r.st.m, a.scale);
-      const Pair s1 = rescaled(in1.x, {in1.y, 0.0f}, r.st.m, a.scale);
-      r.st.s = {warp_sum(s0.hi + s1.hi), warp_sum(s0.lo + s1.lo)};
-      const RowHead& h = heads[slot];
-      const Slice& sl = jobs[slot].slice;
-      const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + sl.count * N;  // the slice's elements
-      const auto mine = [&](int32_t id) {
-        return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
-               (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
-      };
-      r.g = {0.0f, 0.0f};
-      r.writer = -1;
-      r.idle = !r.stop && h.weight == 0.0f;  // a label out of range
-      if (r.idle) {
-        if (lane == 0 && rank == 0) write_idle_row<kMode>(a, t);
-      } else if (!r.stop) {
-        r.g = finish_row<kMode>(a, t, h, r.st, lane == 0 && rank == 0);
-        if (kMode == ROW_POLICY && mine(h.label)) {
-          const int32_t in_slice = h.label - lo_v;
-          r.writer = in_slice / N % kThreads;
-          if (in_slice < 0) r.writer = h.label;                                            // the head
-          else if (h.label >= hi_v) r.writer = sl.edge_count - (a.vocab - h.label);        // the tail
-        }
+      SoftmaxStat st;
+      st.m = warp_max_one(fmaxf(in0.x, in1.x));
+      st.s = rescaled(in0.x, {in0.y, 0.0f}, st.m, a.scale);
+      if (n > 32) {
+        const Pair s1 = rescaled(in1.x, {in1.y, 0.0f}, st.m, a.scale);
+        st.s = {st.s.hi + s1.hi, st.s.lo + s1.lo};
       }
+      st.s = {warp_sum(st.s.hi), warp_sum(st.s.lo)};
+      const RowHead& h = heads[slot];
+      r.m = st.m;
+      r.k = 0.0f;
+      r.idle = h.weight == 0.0f;  // a label out of range
+      PolicyTerms p;
+      if (kMode == ROW_POLICY) {
+        p = policy_terms(a, h, st);
+        r.k = policy_factor(p, st);
+      }
+      if (kMode == ROW_DISTILL) r.k = distill_factor(a, h, st);
       __syncwarp();
       if (lane == 0) {
         results[slot] = r;
@@ -945,9 +922,41 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
         if (r.stop) quit = 1;
       }
       if (r.stop) break;
+      // The rest is not waited for: the scalars, and in the gradient the edges
+      // (the places of the label or the entries among them, and those of the
+      // slice, once the block's warps have written the slice).
+      const Slice& sl = jobs[slot].slice;
+      const int32_t lo_v = sl.head + sl.first * N, hi_v = lo_v + sl.count * N;  // the slice's elements
+      const auto mine = [&](int32_t id) {
+        return (id >= lo_v && id < hi_v) || (rank == 0 && id < sl.head) ||
+               (rank == cluster - 1 && id >= sl.head + (a.vocab - sl.head) / N * N);
+      };
+      const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
+      T* const dz = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
+      const auto write_edges = [&] {
+        if (lane < sl.edge_count) {
+          const int32_t e = edge_index(sl, lane, a.vocab);
+          dz[e] = from_float<T>(Gradient(r.m, r.k, a.scale).of(to_float(z[e]), a.scale));
+        }
+      };
+      if (r.idle) {
+        if (lane == 0 && rank == 0) write_idle_row<kMode>(a, t);
+      } else if (kMode == ROW_SCORE) {
+        if (lane == 0 && rank == 0) write_score(a, t, h, st);
+      } else if (kMode == ROW_POLICY) {
+        if (lane == 0 && rank == 0) write_policy(a, t, h, p);
+        if (dz) {
+          write_edges();
+          if (mine(h.label)) {
+            const float at_label = policy_at_label(p);
+            if (!wait_or_quit(&written[slot], (k / kJobs) & 1, &quit)) break;
+            __syncwarp();
+            if (lane == 0) dz[h.label] = from_float<T>(at_label);
+          }
+        }
+      }
       if (kMode == ROW_DISTILL) {
         const Teacher te = teacher_at(teachers + slot * teacher_bytes(a.teacher_count), a.teacher_count);
-        const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
         const T* const held = reinterpret_cast<const T*>(ring + b * shape.vecs);
         const auto logit = [&](int32_t id) { return to_float(id >= lo_v && id < hi_v ? held[id - lo_v] : z[id]); };
         // the copies have landed, as the statistics show; this warp has to see it for itself
@@ -962,17 +971,11 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
           b = 0;
           phase ^= 1u;
         }
-        const float part = warp_sum(teacher_entries(a, te, h, r.st, lane, 32, mine));
+        const float part = warp_sum(teacher_entries(a, te, h, st, lane, 32, mine));
         if (cluster > 1 && lane == 0)
           cluster_send(&loss_box[got % kJobs][rank], &loss_bar[got % kJobs], 0, make_float2(part, 0.0f));
-        if (a.dlogits) {
-          T* const dz = static_cast<T*>(a.dlogits) + t * a.dstride;
-          // the edges' logits have been read above, whichever matrix they are in
-          if (lane < sl.edge_count) {
-            const int32_t e = edge_index(sl, lane, a.vocab);
-            const Gradient grad(r.st.m, r.g.k, a.scale);
-            dz[e] = from_float<T>(grad.of(to_float(z[e]), a.scale));
-          }
+        if (dz) {
+          write_edges();
           // the entries over the block's own values of the row
           if (!wait_or_quit(&written[slot], (k / kJobs) & 1, &quit)) break;
           __syncwarp();
@@ -1012,7 +1015,6 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ float maxima[kPlainThreads / 32], parts[kPlainThreads / 32];
   __shared__ RowHead head;
-  __shared__ RowResult result;
   __shared__ int32_t stop;
   pdl_wait_then_release();
   const int64_t t = blockIdx.x;
@@ -1060,30 +1062,31 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   SoftmaxStat st = {m, unbiased_sum(group_sum<kPlainThreads>(s, parts))};
   tilt = group_sum<kPlainThreads>(tilt, maxima) * (0.693147181f * (a.scale.lo / a.scale.hi));
   if (fabsf(tilt) < INFINITY) st.s.lo += tilt;
-  if (wid == 0) {
-    RowResult r;
-    r.st = st;
-    r.g = finish_row<kMode>(a, t, h, st, lane == 0);
-    r.writer = -1;
-    r.stop = r.idle = false;
-    if (lane == 0) result = r;
+  if (kMode == ROW_SCORE) {
+    if (tid == 0) write_score(a, t, h, st);
+    return;
   }
-  if (kMode == ROW_SCORE) return;
-  __syncthreads();
-  const RowResult r = result;
+  float k = 0.0f, at_label = 0.0f;
+  if (kMode == ROW_POLICY) {
+    const PolicyTerms p = policy_terms(a, h, st);
+    if (tid == 0) write_policy(a, t, h, p);
+    k = policy_factor(p, st);
+    at_label = policy_at_label(p);
+  }
+  if (kMode == ROW_DISTILL) k = distill_factor(a, h, st);
   const auto all = [](int32_t) { return true; };
   if (kMode == ROW_DISTILL) {
     const auto logit = [&](int32_t id) { return to_float(z[id]); };
     read_entries(a, te, tid, kPlainThreads, all, logit);
-    const float part = group_sum<kPlainThreads>(teacher_entries(a, te, h, r.st, tid, kPlainThreads, all), parts);
+    const float part = group_sum<kPlainThreads>(teacher_entries(a, te, h, st, tid, kPlainThreads, all), parts);
     if (tid == 0) a.token_losses[t] = part * (a.scale.tau * a.scale.tau);
   }
   if (!dz) return;
   __syncthreads();  // every entry's logit is read before the gradient may take its place
-  const Gradient grad(r.st.m, r.g.k, a.scale);
+  const Gradient grad(m, k, a.scale);
   for (uint32_t v = tid; v < V; v += step) {
     float d = grad.of(to_float(z[v]), a.scale);
-    if (kMode == ROW_POLICY && static_cast<int32_t>(v) == h.label) d = r.g.at_label;
+    if (kMode == ROW_POLICY && static_cast<int32_t>(v) == h.label) d = at_label;
     dz[v] = from_float<T>(d);
   }
   if (kMode == ROW_DISTILL) {
