@@ -72,7 +72,7 @@ __device__ __forceinline__ float block_total_pair(Pair p, Pair* tmp) {
 __global__ void __launch_bounds__(kDocThreads)
     count_rows_kernel(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t S, CpMath m, int32_t mult,
                       int32_t* counts, int32_t* st) {
-  pdl_wait_then_release();
+  pdl_wait();
   __shared__ int32_t tmp[32];
   if (block_status_set(st)) return;
   if (blockIdx.x == 0) {
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kDocThreads)
 __global__ void __launch_bounds__(kDocThreads)
     loss_weights_kernel(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t S, CpMath m,
                         int32_t reduction, const int32_t* counts, float* weights, int32_t* doc_ids, const int32_t* st) {
-  pdl_wait_then_release();
+  pdl_wait();
   __shared__ int64_t tmp[32];
   if (block_status_set(st) || n == 0) return;
   int64_t part = 0;
@@ -127,7 +127,7 @@ constexpr int kFewThreads = 1024;
 __global__ void __launch_bounds__(kFewThreads)
     few_weights_kernel(const uint8_t* mask, const int32_t* cu, int32_t n, int32_t T, int32_t S, CpMath m, int32_t mult,
                        int32_t reduction, float* weights, int32_t* doc_ids, int32_t* st) {
-  pdl_wait_then_release();
+  pdl_wait();
   __shared__ int32_t bounds[kFewDocs + 1], counts[kFewDocs];
   __shared__ int32_t tmp[32];
   if (block_status_set(st)) return;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kFewThreads)
 // over the reference: one block per document.
 __global__ void __launch_bounds__(kDocThreads)
     doc_sums_kernel(const PreferenceArgs a, int32_t S, CpMath m, int32_t mult) {
-  pdl_wait_then_release();
+  pdl_wait();
   __shared__ Pair pairs[32];
   __shared__ int32_t tmp[32];
   if (block_status_set(a.status)) return;
@@ -250,7 +250,7 @@ __device__ __forceinline__ bool pair_ok(const PreferenceArgs& a, int32_t c, int3
 // Blocks 0 .. num_docs-1: one document's gradient from every pair it is in,
 // then its rows' gradients.  The last block: every pair's margin and the loss.
 __global__ void __launch_bounds__(kDocThreads) preference_kernel(const PreferenceArgs a, int32_t S, CpMath m) {
-  pdl_wait_then_release();
+  pdl_wait();
   __shared__ Pair pairs[32];
   if (block_status_set(a.status)) return;
   const float each = a.num_pairs > 0 ? 1.0f / static_cast<float>(a.num_pairs) : 0.0f;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kDocThreads) preference_kernel(const Preferenc
 // out[k] = sum of a[k][t] * b[t], one block per k, the same order in every run.
 __global__ void __launch_bounds__(kSumThreads)
     final_sums_kernel(const float* a, const float* b, int64_t n, float* out, const int32_t* st) {
-  pdl_wait_then_release();
+  pdl_wait();
   __shared__ Pair pairs[32];
   if (block_status_set(st)) return;
   const float* v = a + blockIdx.x * n;

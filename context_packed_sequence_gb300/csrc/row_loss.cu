@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 96, kPerSm)
     }
     mbar_init_fence();
   }
-  pdl_wait_then_release();
+  pdl_wait();
   if (tid == 0 && rank == 0) stop = status_load(a.status);
   if (cluster > 1) cluster_sync();
   if (tid == 0 && rank != 0) stop = cluster_load0(&stop);
@@ -1016,7 +1016,7 @@ __global__ void __launch_bounds__(kPlainThreads) row_plain_kernel(const __grid_c
   __shared__ float maxima[kPlainThreads / 32], parts[kPlainThreads / 32];
   __shared__ RowHead head;
   __shared__ int32_t stop;
-  pdl_wait_then_release();
+  pdl_wait();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -1224,7 +1224,7 @@ __global__ void __launch_bounds__(kBackThreads)
                              int32_t tiles) {
   constexpr int N = Word<T>::kElems;
   constexpr int kStep = kBackThreads * kVecsPerStep;
-  pdl_wait_then_release();
+  pdl_wait();
   const int tid = threadIdx.x;
   const uint32_t from_last = blockIdx.x / static_cast<uint32_t>(tiles);
   const int64_t t = a.rows - 1 - static_cast<int32_t>(from_last);

@@ -401,8 +401,9 @@ int sm_count();
 // Every kernel of this library is launched with programmatic stream
 // serialization: it may be scheduled while the previous kernel on the stream
 // is still finishing, which hides the launch gap between back-to-back
-// kernels.  Each kernel's first statement is pdl_wait_then_release()
-// (tma.cuh), so it touches memory only after its predecessor has completed.
+// kernels.  Each kernel's first statement is pdl_wait_then_release() or
+// pdl_wait() (tma.cuh), so it touches memory only after its predecessor has
+// completed.
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args... args) {
