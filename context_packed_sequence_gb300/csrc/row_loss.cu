@@ -10,16 +10,19 @@
 //
 // Bytes bound all of it: a row of V logits of e bytes cannot do with less than
 // V e read and V e written.  Measured (one GB300, copy bandwidth 6,775 GB/s,
-// rows of 151936 bf16, inputs larger than the L2):
-//   log-probabilities, 8192 rows                377 us  6.61 TB/s  98 %
+// rows of 151936 bf16, inputs larger than the L2, call after call):
+//   log-probabilities, 8192 rows                356 us  6.98 TB/s 103 %
 //   policy loss with its gradient, 8192 rows, 30 % without loss, with the row
-//   weights and the final sums                  685 us  6.18 TB/s  91 %
+//   weights and the final sums                  659 us  6.42 TB/s  95 %
 //   distillation from 64 entries with its gradient, 4096 rows, 20 % without
-//                                               417 us  5.37 TB/s  79 %
+//   loss, with the row weights                  379 us  5.92 TB/s  87 %
 // What keeps the last two from the bandwidth is the time between a slice's
-// last byte and its first gradient (its sum, the exchange, the row's scalars:
-// about 4 us), in which the other blocks of the SM have to keep the memory
-// busy: with both sweeps' arithmetic taken out they run at 94 %.
+// last byte and its first gradient (its sum, the exchange, the row's scalars),
+// in which the other blocks of the SM have to keep the memory busy, and the
+// first and last rows of a launch.  The code counts there, not the arithmetic:
+// every warp is somewhere else in it, and instructions that are not in the
+// cache are waited for.  Loops of the serving warps are therefore not
+// unrolled, and what no other warp waits for comes after what one does.
 #include <algorithm>
 
 #include "loss_internal.cuh"
@@ -1109,15 +1112,18 @@ constexpr int64_t kBlockShared = 1024 + 2304;
 constexpr int64_t block_budget(int n) { return kSmShared / n - kBlockShared; }
 // Below this a slice is not divided further for want of rows.
 constexpr int64_t kSmallestSlice = 8 * 1024;
-// Slices up to this are taken by blocks of 4 warps, larger ones by 8.
+// Slices up to this are taken by blocks of 4 warps, four on an SM, larger ones
+// by 8 (8192 rows of 8192 bf16, policy loss: 69 us, with 8 warps 82; of 32768,
+// 64 KiB: 177 us either way).
 constexpr int64_t kSmallSlice = 32 * 1024;
 // Rows a cluster takes at a time, where there are enough of them: the loads of
-// their scalars wait for one another (2 to 3 us), which a row shorter than
-// that would feel.  Rows of kLongRow bytes and a gradient take longer and are
-// taken one by one, for the balance (8192 rows of 151936 bf16, a third of them
-// without loss: 685 us, by fours 700; log-probabilities of 4096 such rows by
-// fours, with their gradient 448 us, one by one 457).
-constexpr int32_t kGroup = 4;
+// their scalars wait for one another (2 to 3 us), which a short row would feel
+// (log-probabilities of 8192 rows of 16384 bf16: 49 us, one by one 57), and
+// rows taken together are less even a share (a preference step over 4096 rows
+// of 151936 bf16: 424 us, by fours 428).  Rows of kLongRow bytes and a gradient
+// take long enough alone (policy loss of 8192 of them, a third without loss:
+// 659 us, by twos 661, by fours 672).
+constexpr int32_t kGroup = 2;
 constexpr int64_t kLongRow = 256 * 1024;
 
 template <typename T, int kMode, int kWarps, int kPerSm>
@@ -1157,14 +1163,15 @@ thd_status_t launch_cluster(const RowArgs& a, RingShape shape, int64_t slice, in
 //
 // Three blocks on an SM hide one another's waits (for logits, for the other
 // blocks of the cluster) better than two; a row shared by more blocks pays
-// more exchanges and more work per row.  Shares of the copy bandwidth, policy
-// loss over bf16 rows: vocabulary 32768, one block a row, three on an SM 85 %,
-// two 75 %; 65536, two a row, 88 and 80 %; 100352, three a row and an SM 79 %,
-// two a row and an SM 87 %; 151936, five a row and three an SM 80 %, three a
-// row and two an SM 82 %.  So two on an SM where that takes fewer a row.  The
-// log-probabilities alone, which write nothing, take three on an SM wherever
-// they fit (131072: 98 and 88 %; 2049 rows of 50257 f16 with their backward
-// pass 90 and 99 us).
+// more exchanges and more work per row.  With a gradient, two on an SM where
+// that takes fewer a row and the SM's blocks hold as many bytes of rows
+// together, give or take 5 %.  Shares of the copy bandwidth of the policy loss
+// (a distillation) over bf16 rows, two and three on an SM: vocabulary 151936,
+// three and five blocks a row, 92 and 90 % (90 and 82); 131072, three and four,
+// 89 and 96 % (85 and 90); 100352, two and three, 93 and 89 % (93 and 81);
+// 65536, two either way, 85 and 96 % (84 and 92).  The log-probabilities alone,
+// which write nothing, take three on an SM wherever they fit (151936: 94 and
+// 99 %; 131072: 93 and 104; but 100352: 96 and 91).
 template <typename T, int kMode>
 thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
@@ -1178,7 +1185,7 @@ thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
     return cluster;  // kMaxCluster + 1: none
   };
   const int32_t by3 = least(block_budget(3)), by2 = least(block_budget(2));
-  const bool two = by2 < by3 && (kMode != ROW_SCORE || by3 > kMaxCluster);
+  const bool two = by3 > kMaxCluster || (kMode != ROW_SCORE && by2 < by3 && 42 * slice_of(by2) >= 60 * slice_of(by3));
   const int32_t per_sm = by2 > kMaxCluster ? 1 : two ? 2 : 3;
   RingShape shape;
   shape.cluster = per_sm == 3 ? by3 : per_sm == 2 ? by2 : kMaxCluster;
