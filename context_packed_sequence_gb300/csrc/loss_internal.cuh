@@ -209,8 +209,9 @@ __device__ __forceinline__ float warp_max(float v) {
 // hashed to, in the memory of z, which is filled later, and reads back whose
 // number stayed: its own, another one's with the same id, or that of another
 // id, which it tries elsewhere.  Entries with one id go the same way, so one
-// of them finds the other.  Comparing each with each instead took 0.6 us a
-// row for 64 entries and 40 us for 512.
+// of them finds the other.  Comparing each with each instead:
+// 4096 rows of 151936 bf16 with 128 entries 449 us, not 431; with 512 1871, not
+// 745.
 __device__ __forceinline__ bool ids_repeat(const Teacher& s, int32_t count) {
   const int lane = threadIdx.x & 31;
   if (count <= 32) {

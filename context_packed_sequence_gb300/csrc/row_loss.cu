@@ -1163,15 +1163,18 @@ thd_status_t launch_cluster(const RowArgs& a, RingShape shape, int64_t slice, in
 //
 // Three blocks on an SM hide one another's waits (for logits, for the other
 // blocks of the cluster) better than two; a row shared by more blocks pays
-// more exchanges and more work per row.  With a gradient, two on an SM where
-// that takes fewer a row and the SM's blocks hold as many bytes of rows
-// together, give or take 5 %.  Shares of the copy bandwidth of the policy loss
-// (a distillation) over bf16 rows, two and three on an SM: vocabulary 151936,
-// three and five blocks a row, 92 and 90 % (90 and 82); 131072, three and four,
-// 89 and 96 % (85 and 90); 100352, two and three, 93 and 89 % (93 and 81);
-// 65536, two either way, 85 and 96 % (84 and 92).  The log-probabilities alone,
-// which write nothing, take three on an SM wherever they fit (151936: 94 and
-// 99 %; 131072: 93 and 104; but 100352: 96 and 91).
+// more exchanges and more work per row.  So two on an SM where that takes fewer
+// a row and the SM's blocks hold as many bytes of rows together, give or take
+// 5 %.  Shares of the copy bandwidth, bf16, two and three on an SM, of the policy
+// loss / a distillation / the log-probabilities:
+//   151936, 3 and 5 blocks a row   92  90   90  82   94  99
+//   131072, 3 and 4                89  96   85  90   93 104
+//   100352, 2 and 3                93  89   93  81   96  92
+//    65536, 2 either way           85  96   84  92   99 104
+//    40000, 1 and 2                90  76   88  70   96  79
+// The log-probabilities alone have no gradient to hold a row for, and lose less
+// by sharing: three on an SM for them also where two would take three a row or
+// more.
 template <typename T, int kMode>
 thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
   const int64_t row = static_cast<int64_t>(a.vocab) * sizeof(T);
@@ -1185,7 +1188,8 @@ thd_status_t launch_mode(const RowArgs& a, cudaStream_t s) {
     return cluster;  // kMaxCluster + 1: none
   };
   const int32_t by3 = least(block_budget(3)), by2 = least(block_budget(2));
-  const bool two = by3 > kMaxCluster || (kMode != ROW_SCORE && by2 < by3 && 42 * slice_of(by2) >= 60 * slice_of(by3));
+  const bool two = by3 > kMaxCluster || (by2 < by3 && 42 * slice_of(by2) >= 60 * slice_of(by3) &&
+                                         (kMode != ROW_SCORE || by2 <= 2));
   const int32_t per_sm = by2 > kMaxCluster ? 1 : two ? 2 : 3;
   RingShape shape;
   shape.cluster = per_sm == 3 ? by3 : per_sm == 2 ? by2 : kMaxCluster;

@@ -665,6 +665,26 @@ def test_the_loss_alone_is_the_loss_with_a_gradient(T, V, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("T,V,dtype", [(500, 151936, BF16), (700, 50257, F16), (400, 32003, F32), (2000, 1000, BF16)])
+def test_gradients_of_many_rows_in_place(T, V, dtype):
+    """Rows shared by several blocks, the next ones fetched while a gradient replaces the logits: the bits of a gradient
+    elsewhere.  Labels at the ends and within every block's part."""
+    z, _ = make_logits(T + 1, T, V, dtype)
+    y = (torch.arange(T, device="cuda") * 7919 % V).to(torch.int32)
+    y[::5], y[1::5] = 0, V - 1
+    g = np.random.default_rng(V)
+    f = lambda a: dev(a, F32)  # noqa: E731
+    w, old, A = f(g.random(T) * (g.random(T) < 0.8)), f(g.standard_normal(T) - 8), f(g.standard_normal(T))
+    ids, sc = dev(g.integers(0, V, (T, 20)), torch.int32), f(g.standard_normal((T, 20)))
+    lse = thd.token_logprobs(z, y)[1]
+    for call in (lambda x, **kw: thd.token_logprobs_backward(x, y, lse, w, **kw),
+                 lambda x, **kw: thd.policy_loss(x, y, w, old, A, **kw).dlogits,
+                 lambda x, **kw: thd.distill_topk_loss(x, ids, sc, w, **kw).dlogits):
+        want, over = call(z), z.clone()
+        assert torch.equal(call(over, out=over), want)
+
+
+@gpu
 def test_distill_gradient_is_the_losses_difference():
     """As for the policy loss: a directional difference within 2e-3."""
     T, V, K = 6, 300, 12
