@@ -8,10 +8,6 @@ namespace thd {
 
 enum RowMode { ROW_SCORE = 0, ROW_POLICY = 1, ROW_DISTILL = 2 };
 
-// Teacher entries a row may have (thd_distill_topk_loss); the row's entries
-// are held in shared memory.
-constexpr int kMaxTeacher = THD_MAX_TEACHER_ENTRIES;
-
 struct RowArgs {
   const void* logits;
   int64_t stride;   // elements between rows

@@ -549,8 +549,8 @@ struct RowJob {
 // Three more serve them.  One finds the next rows and reads what they need
 // besides their logits.  One fetches the slices into a ring of buffers, chunk
 // by chunk as they become free.  One joins the statistics, which every warp of
-// every block of the cluster sends to every block, and finishes the row's
-// scalars and a teacher's entries.  No barrier of the block is waited at: a
+// every block of the cluster sends to every block, releases the row's
+// gradient, and finishes the scalars, the label and a teacher's entries.  No barrier of the block is waited at: a
 // warp that gives up waiting tells the others and leaves.
 //
 // Statistics of row n (rows with weight counted) go to box n % 2.  A warp
