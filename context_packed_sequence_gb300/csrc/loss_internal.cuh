@@ -165,7 +165,9 @@ struct Teacher {
   float* lq;    // logarithm of it
   float* z;     // the student's logit; later the gradient in the entry's place
 };
-constexpr int kEntryBatch = 4;  // loads of each kind in flight a lane
+// Loads of each kind in flight a lane: 4096 rows of 151936 bf16 with 512 entries
+// 691 us, by fours 760; with 64 entries 406 either way, by sixteens 414.
+constexpr int kEntryBatch = 8;
 constexpr int kHashRounds = 6;  // 1024 different ids: 0.2, 0.02 and 1e-4 of them are left after 1, 2 and 3
 
 __host__ __device__ __forceinline__ int32_t teacher_slots(int32_t count) { return (count + 3) & ~3; }
